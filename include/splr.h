@@ -19,7 +19,8 @@
  *    the error code is returned.  A failed launch returns SPLR_ERR_HIP.  No C++ exception crosses
  *    the boundary.
  *  - Storage types: SPLR_FP32 = IEEE binary32, SPLR_BF16 = bfloat16 (upper half of a binary32).
- *    The same dtype applies to every floating-point input of one call; Y and W_hat are float32.
+ *    The same dtype applies to every floating-point input of one call unless an entry point says
+ *    otherwise; Y and W_hat are float32 unless the call has a y_dtype.
  *  - n_in must be a positive multiple of 32 (a metadata word covers 32 input columns).
  *
  * Packed 2:4 layout (shared by every entry point)
@@ -57,6 +58,15 @@ extern "C" {
 #endif
 
 typedef enum { SPLR_FP32 = 0, SPLR_BF16 = 1 } splr_dtype_t;
+
+/* Activations of splr_epilogue_t, evaluated in float32. */
+typedef enum {
+  SPLR_ACT_NONE = 0,      /* z                                                                   */
+  SPLR_ACT_RELU = 1,      /* max(z, 0), NaN stays NaN                                            */
+  SPLR_ACT_GELU = 2,      /* z (1 + erf(z / sqrt 2)) / 2                                         */
+  SPLR_ACT_GELU_TANH = 3, /* z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2                   */
+  SPLR_ACT_SILU = 4       /* z / (1 + exp(-z))                                                   */
+} splr_activation_t;
 
 typedef enum {
   SPLR_OK = 0,
@@ -314,6 +324,78 @@ splr_status_t splr_linear_stage2_group(int32_t count, const void* const* X, int6
 splr_status_t splr_linear_noalloc(const void* X, int64_t M, int64_t n_in, const void* values,
                                   const uint32_t* meta, int64_t n_out, const void* U, const void* V,
                                   int64_t r, splr_dtype_t dtype, float* Y, hipStream_t stream);
+
+/*
+ * splr_linear_fused -- the layer product with the work a transformer block does on its result in the
+ * epilogue:
+ *
+ *     Z = X S^T + (X V^T) U^T + bias          Y = act(Z) * gate + residual
+ *
+ * (LoSparse page, section 3.2, for the two products).  Everything after the products is evaluated in
+ * float32 and rounded once, to y_dtype, when Y is stored, so no intermediate matrix goes to memory.
+ *
+ *   X, values, meta, U, V, r, workspace          as for splr_linear
+ *   epilogue   NULL, or the operands below; a NULL operand is left out
+ *     activation   act, applied to Z
+ *     bias         [n_out] dtype, added to every row
+ *     gate         [M][n_out] y_dtype, multiplied onto act(Z) (e.g. the up projection's output)
+ *     residual     [M][n_out] y_dtype, added last
+ *   Y          [M][n_out] y_dtype.  It may be the very buffer of gate or of residual (same address:
+ *              every entry is read before it is written); it must not overlap anything else.
+ * Arithmetic: float32 accumulation as splr_linear; bitwise reproducible run to run.
+ * Errors: as splr_linear_ex; epilogue operands misaligned -> SPLR_ERR_ALIGN; activation unknown ->
+ *         SPLR_ERR_SHAPE.
+ */
+typedef struct {
+  splr_activation_t activation;
+  const void* bias;
+  const void* gate;
+  const void* residual;
+} splr_epilogue_t;
+
+splr_status_t splr_linear_fused(const void* X, int64_t M, int64_t n_in, const void* values,
+                                const uint32_t* meta, int64_t n_out, const void* U, const void* V,
+                                int64_t r, splr_dtype_t dtype, const splr_epilogue_t* epilogue,
+                                splr_dtype_t y_dtype, void* Y, void* workspace,
+                                size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * splr_linear_experts -- splr_linear_fused for rows grouped by expert (a mixture of compressed
+ * experts of one shape): row m of X, gate, residual and Y with offsets[e] <= m < offsets[e+1] goes
+ * through expert e,
+ *
+ *     Y[m] = act(X[m] S_e^T + (X[m] V_e^T) U_e^T + bias_e) * gate[m] + residual[m].
+ *
+ * The group sizes stay on the device: the kernels read `offsets`, the host neither waits for them
+ * nor copies them, so a captured call may be replayed with other offsets.
+ *
+ *   X          [M][n_in] dtype                  rows sorted by expert
+ *   offsets    [n_experts + 1] int32 (device, 4-byte aligned), non-decreasing, within 0 .. M.  Groups
+ *              may be empty.  Rows before offsets[0] and from offsets[n_experts] on belong to no
+ *              expert: they are not computed and their Y is left as it was.
+ *              Offsets that break these rules give unspecified rows of Y, but nothing outside the
+ *              arguments' buffers is read or written.
+ *   values, meta   the experts' packed S, one after the other (splr_packed_bytes apart)
+ *   U [n_experts][n_out][r], V [n_experts][r][n_in] dtype (NULL iff r == 0)
+ *   epilogue   as splr_linear_fused, bias [n_experts][n_out]
+ *   Y          as splr_linear_fused
+ *   workspace  splr_linear_experts_workspace_bytes() bytes (0 when r == 0), clobbered; its contents
+ *              on entry do not matter.  Two calls that may run at the same time need one each.
+ * M may be 0 (no row was routed here): nothing is enqueued and X, gate, residual and Y may be NULL.
+ * Arithmetic: as splr_linear_fused; a row's result depends on its own row and its expert only,
+ * except for the order of the float32 sums, which follows the kernel that M and n_experts select.
+ * Errors: as splr_linear_fused; n_experts outside 1 .. SPLR_EXPERTS_MAX, or n_experts * n_out * n_in
+ *         above 2^36 -> SPLR_ERR_SHAPE.
+ */
+#define SPLR_EXPERTS_MAX 1024
+size_t splr_linear_experts_workspace_bytes(int64_t M, int64_t n_experts, int64_t n_out, int64_t n_in,
+                                           int64_t r, splr_dtype_t dtype);
+splr_status_t splr_linear_experts(const void* X, int64_t M, int64_t n_in, const int32_t* offsets,
+                                  int64_t n_experts, const void* values, const uint32_t* meta,
+                                  int64_t n_out, const void* U, const void* V, int64_t r,
+                                  splr_dtype_t dtype, const splr_epilogue_t* epilogue,
+                                  splr_dtype_t y_dtype, void* Y, void* workspace,
+                                  size_t workspace_bytes, hipStream_t stream);
 
 /*
  * splr_dense_reconstruct -- W_hat = S + U V as a dense float32 matrix (LoSparse §3: the weight is

@@ -13,6 +13,7 @@ explicitly where it cannot be read off U.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import List, Optional, Sequence, Tuple
@@ -27,7 +28,8 @@ STATUS = {0: "SPLR_OK", 1: "SPLR_ERR_NULL", 2: "SPLR_ERR_SHAPE", 3: "SPLR_ERR_DT
           5: "SPLR_ERR_HIP", 6: "SPLR_ERR_WORKSPACE", 7: "SPLR_ERR_SCRATCH"}
 EXPORTS = ("splr_prune24_pack", "splr_prune_nm_pack", "splr_linear_ex", "splr_prune24_pack_scaled", "splr_prune24_pack_residual", "splr_packed_bytes", "splr_linear_workspace_bytes", "splr_linear",
            "splr_linear_stage1", "splr_linear_stage2", "splr_linear_stage2_dense", "splr_linear_group",
-           "splr_linear_stage2_group", "splr_linear_noalloc", "splr_dense_reconstruct",
+           "splr_linear_stage2_group", "splr_linear_noalloc", "splr_linear_fused", "splr_linear_experts",
+           "splr_linear_experts_workspace_bytes", "splr_dense_reconstruct",
            "splr_gram_workspace_bytes", "splr_gram_f64", "splr_chol_rinv", "splr_status_string", "splr_version")
 
 _P, _I64, _I32, _SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t
@@ -75,6 +77,13 @@ def lib() -> ctypes.CDLL:
         L.splr_linear_stage2_group.restype = _I32
         L.splr_linear_noalloc.argtypes = [_P, _I64, _I64, _P, _P, _I64, _P, _P, _I64, _I32, _P, _P]
         L.splr_linear_noalloc.restype = _I32
+        L.splr_linear_fused.argtypes = [_P, _I64, _I64, _P, _P, _I64, _P, _P, _I64, _I32, _P, _I32, _P, _P, _SZ, _P]
+        L.splr_linear_fused.restype = _I32
+        L.splr_linear_experts_workspace_bytes.argtypes = [_I64, _I64, _I64, _I64, _I64, _I32]
+        L.splr_linear_experts_workspace_bytes.restype = _SZ
+        L.splr_linear_experts.argtypes = [_P, _I64, _I64, _P, _I64, _P, _P, _I64, _P, _P, _I64, _I32, _P, _I32, _P,
+                                          _P, _SZ, _P]
+        L.splr_linear_experts.restype = _I32
         L.splr_dense_reconstruct.argtypes = [_P, _P, _P, _P, _I64, _I64, _I64, _I32, _P, _P]
         L.splr_dense_reconstruct.restype = _I32
         L.splr_gram_workspace_bytes.argtypes = [_I64, _I64]
@@ -466,6 +475,116 @@ def linear_noalloc(X: torch.Tensor, values: torch.Tensor, meta: torch.Tensor, U:
            lib().splr_linear_noalloc(_dev(X, "X"), M, n_in, _dev(values, "values"), _dev(meta, "meta"), n_out,
                                      _dev(U, "U"), _dev(V, "V"), r, _dtype_code(X), _dev(out, "out"),
                                      _stream(stream)))
+    return out
+
+
+ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}  # splr_activation_t
+EXPERTS_MAX = 1024  # SPLR_EXPERTS_MAX
+
+
+class _Epilogue(ctypes.Structure):
+    """splr_epilogue_t."""
+    _fields_ = [("activation", _I32), ("bias", _P), ("gate", _P), ("residual", _P)]
+
+
+def _epilogue(X, M, n_out, bias, bias_shape, activation, gate, residual, y_dtype):
+    """Checks the epilogue's operands and returns them as the C struct."""
+    if activation not in ACTIVATIONS:
+        raise ValueError(f"activation must be one of {', '.join(ACTIVATIONS)}, got {activation!r}")
+    if y_dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"y_dtype must be float32 or bfloat16, got {y_dtype}")
+    if bias is not None:
+        _expect(bias, "bias", X.dtype, bias.numel(), X.device, bias_shape)
+    for t, name in ((gate, "gate"), (residual, "residual")):
+        if t is not None:
+            _expect(t, name, y_dtype, M * n_out, X.device, (M, n_out))
+    return _Epilogue(ACTIVATIONS[activation], _dev(bias, "bias"), _dev(gate, "gate"), _dev(residual, "residual"))
+
+
+def _on_device_of(t: torch.Tensor):
+    """The device of `t` made current for the call: its streams and launches belong to it."""
+    return torch.cuda.device(t.device) if t.is_cuda else contextlib.nullcontext()
+
+
+def linear_fused(X: torch.Tensor, values: torch.Tensor, meta: torch.Tensor, U: Optional[torch.Tensor],
+                 V: Optional[torch.Tensor], bias: Optional[torch.Tensor] = None, activation: str = "none",
+                 gate: Optional[torch.Tensor] = None, residual: Optional[torch.Tensor] = None,
+                 y_dtype: torch.dtype = torch.float32, n_out: Optional[int] = None,
+                 out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                 stream=None) -> torch.Tensor:
+    """Y [M, n_out] of y_dtype = act(X S^T + (X V^T) U^T + bias) * gate + residual, with everything
+    after the products in the kernels' epilogue (splr_linear_fused). bias [n_out] of X's type; gate
+    and residual [M, n_out] of y_dtype; `out` may be gate or residual itself. The workspace is
+    linear's (new_workspace)."""
+    M, n_in = _matrix(X, "X")
+    with _on_device_of(X):
+        M, n_in, n_out, r, out, workspace, ws_bytes = _linear_args(X, values, meta, U, V, n_out, out, workspace,
+                                                                   stream, y_dtype=y_dtype)
+        ep = _epilogue(X, M, n_out, bias, (n_out,), activation, gate, residual, y_dtype)
+        ycode = SPLR_BF16 if y_dtype == torch.bfloat16 else SPLR_FP32
+        _check("splr_linear_fused",
+               lib().splr_linear_fused(_dev(X, "X"), M, n_in, _dev(values, "values"), _dev(meta, "meta"), n_out,
+                                       _dev(U, "U"), _dev(V, "V"), r, _dtype_code(X), ctypes.byref(ep), ycode,
+                                       _dev(out, "out"), _dev(workspace, "workspace"), ws_bytes, _stream(stream)))
+    return out
+
+
+def experts_workspace_bytes(M: int, n_experts: int, n_out: int, n_in: int, r: int, dtype: torch.dtype) -> int:
+    code = SPLR_BF16 if dtype == torch.bfloat16 else SPLR_FP32
+    return int(lib().splr_linear_experts_workspace_bytes(M, n_experts, n_out, n_in, r, code))
+
+
+def linear_experts(X: torch.Tensor, offsets: torch.Tensor, values: torch.Tensor, meta: torch.Tensor,
+                   U: Optional[torch.Tensor], V: Optional[torch.Tensor], bias: Optional[torch.Tensor] = None,
+                   activation: str = "none", gate: Optional[torch.Tensor] = None,
+                   residual: Optional[torch.Tensor] = None, y_dtype: torch.dtype = torch.float32,
+                   n_out: Optional[int] = None, out: Optional[torch.Tensor] = None,
+                   workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """linear_fused for rows grouped by expert (splr_linear_experts): rows offsets[e] .. offsets[e+1]-1
+    of X, gate, residual and Y go through expert e's packed S, U, V and bias.
+
+    offsets: int32 [E + 1] on the device, non-decreasing, within 0 .. M; it is read by the kernels
+    only, so nothing waits for it. values (E, TR, TK, 64, 8) and meta (E, TR, TKB, 64, 4): the experts'
+    packed S one after the other; U [E, n_out, r], V [E, r, n_in], bias [E, n_out]. M may be 0. Rows
+    outside offsets[0] .. offsets[E]-1 of `out` are left as they were."""
+    M, n_in = _matrix(X, "X")
+    _dtype_code(X)
+    if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1 or not 2 <= offsets.numel() <= EXPERTS_MAX + 1:
+        raise ValueError(f"offsets must be a vector of 2 .. {EXPERTS_MAX + 1} entries")
+    E = offsets.numel() - 1
+    _expect(offsets, "offsets", torch.int32, E + 1, X.device)
+    if n_out is None:
+        n_out = U.shape[1] if U is not None and U.dim() == 3 else values.shape[1] * 16
+    TR, TK = tiles(n_out, n_in)
+    _expect(values, "values", X.dtype, E * TR * TK * 512, X.device)
+    _expect(meta, "meta", torch.int32, E * _meta_words(n_out, n_in), X.device)
+    if (U is None) != (V is None):
+        raise ValueError("U and V are given together (or neither, for no low-rank part)")
+    r = 0
+    if U is not None:
+        r = U.shape[2] if U.dim() == 3 else -1
+        _expect(U, "U", X.dtype, E * n_out * max(r, 0), X.device, (E, n_out, r))
+        _expect(V, "V", X.dtype, E * max(r, 0) * n_in, X.device, (E, r, n_in))
+    ep = _epilogue(X, M, n_out, bias, (E, n_out), activation, gate, residual, y_dtype)
+    with _on_device_of(X):
+        need = experts_workspace_bytes(M, E, n_out, n_in, r, X.dtype)
+        if out is None or (workspace is None and need):
+            with torch.cuda.stream(_the_stream(stream)):
+                if out is None:
+                    out = torch.empty((M, n_out), dtype=y_dtype, device=X.device)
+                if workspace is None and need:
+                    workspace = torch.empty(need, dtype=torch.uint8, device=X.device)
+        _expect(out, "out", y_dtype, M * n_out, X.device, (M, n_out))
+        if workspace is not None and (not _is_device(workspace) or workspace.device != X.device
+                                      or not workspace.is_contiguous()):
+            raise ValueError("workspace must be a contiguous tensor on the device of X")
+        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        ycode = SPLR_BF16 if y_dtype == torch.bfloat16 else SPLR_FP32
+        _check("splr_linear_experts",
+               lib().splr_linear_experts(_dev(X, "X"), M, n_in, _dev(offsets, "offsets"), E, _dev(values, "values"),
+                                         _dev(meta, "meta"), n_out, _dev(U, "U"), _dev(V, "V"), r, _dtype_code(X),
+                                         ctypes.byref(ep), ycode, _dev(out, "out"), _dev(workspace, "workspace"),
+                                         ws_bytes, _stream(stream)))
     return out
 
 

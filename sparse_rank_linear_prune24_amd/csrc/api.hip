@@ -283,6 +283,88 @@ splr_status_t splr_linear_group(int32_t count, const void* const* X, int64_t M, 
 
 }  // extern "C"
 
+// ---------------------------------------------------------------- fused epilogue, experts
+namespace {
+
+// Checks the epilogue and turns it into the kernels' form.
+splr_status_t check_epilogue(const splr_epilogue_t* epilogue, splr_dtype_t dtype, splr_dtype_t y_dtype,
+                             splr::Epilogue* out) {
+  if (!dtype_ok(y_dtype)) return SPLR_ERR_DTYPE;
+  *out = splr::Epilogue{nullptr, nullptr, nullptr, splr::kActNone, dtype == SPLR_BF16 ? 1 : 0};
+  if (!epilogue) return SPLR_OK;
+  const int act = (int)epilogue->activation;
+  if (act < 0 || act >= splr::kActCount) return SPLR_ERR_SHAPE;
+  if (!aligned16(epilogue->bias) || !aligned16(epilogue->gate) || !aligned16(epilogue->residual))
+    return SPLR_ERR_ALIGN;
+  out->bias = epilogue->bias;
+  out->gate = epilogue->gate;
+  out->residual = epilogue->residual;
+  out->act = act;
+  return SPLR_OK;
+}
+
+size_t experts_workspace_bytes(int64_t M, int64_t r) {
+  return r == 0 ? 0 : round_up(splr::fused_workspace_bytes(M, r), 256);
+}
+
+}  // namespace
+
+extern "C" {
+
+splr_status_t splr_linear_fused(const void* X, int64_t M, int64_t n_in, const void* values, const uint32_t* meta,
+                                int64_t n_out, const void* U, const void* V, int64_t r, splr_dtype_t dtype,
+                                const splr_epilogue_t* epilogue, splr_dtype_t y_dtype, void* Y, void* workspace,
+                                size_t ws_bytes, hipStream_t stream) {
+  splr_status_t s = check_linear(X, M, n_in, values, meta, n_out, U, V, r, dtype, Y, workspace, ws_bytes, true, true);
+  if (s != SPLR_OK) return s;
+  splr::Epilogue ep;
+  s = check_epilogue(epilogue, dtype, y_dtype, &ep);
+  if (s != SPLR_OK) return s;
+  return from_hip(splr::launch_fused(X, M, n_in, nullptr, 1, values, meta, n_out, U, V, r, dtype == SPLR_BF16, ep, Y,
+                                     y_dtype == SPLR_BF16, workspace, stream));
+}
+
+size_t splr_linear_experts_workspace_bytes(int64_t M, int64_t n_experts, int64_t n_out, int64_t n_in, int64_t r,
+                                           splr_dtype_t dtype) {
+  (void)n_out;
+  if (M < 0 || M > kMaxRows || n_experts < 1 || n_experts > SPLR_EXPERTS_MAX || check_in(n_in) != SPLR_OK ||
+      check_rank(r) != SPLR_OK || !dtype_ok(dtype))
+    return 0;
+  return experts_workspace_bytes(M, r);
+}
+
+splr_status_t splr_linear_experts(const void* X, int64_t M, int64_t n_in, const int32_t* offsets, int64_t n_experts,
+                                  const void* values, const uint32_t* meta, int64_t n_out, const void* U,
+                                  const void* V, int64_t r, splr_dtype_t dtype, const splr_epilogue_t* epilogue,
+                                  splr_dtype_t y_dtype, void* Y, void* workspace, size_t ws_bytes,
+                                  hipStream_t stream) {
+  if (!offsets || !values || !meta || (r > 0 && (!U || !V))) return SPLR_ERR_NULL;
+  if (M != 0 && (!X || !Y)) return SPLR_ERR_NULL;
+  splr_status_t s = check_in(n_in);
+  if (s == SPLR_OK && (M < 0 || n_experts < 1 || n_experts > SPLR_EXPERTS_MAX)) s = SPLR_ERR_SHAPE;
+  if (s == SPLR_OK && M > 0) s = check_rows(M, n_in);
+  if (s == SPLR_OK) s = check_rows(n_out, n_in);
+  if (s == SPLR_OK && n_experts * n_out * n_in > kMaxElems) s = SPLR_ERR_SHAPE;
+  if (s == SPLR_OK) s = check_rank(r);
+  if (s == SPLR_OK && M * n_out > kMaxElems) s = SPLR_ERR_SHAPE;
+  if (s != SPLR_OK) return s;
+  if (!dtype_ok(dtype)) return SPLR_ERR_DTYPE;
+  splr::Epilogue ep;
+  s = check_epilogue(epilogue, dtype, y_dtype, &ep);
+  if (s != SPLR_OK) return s;
+  if (!aligned16(X) || !aligned16(values) || !aligned16(meta) || !aligned16(Y) ||
+      (reinterpret_cast<uintptr_t>(offsets) & 3u) || (r > 0 && (!aligned16(U) || !aligned16(V))))
+    return SPLR_ERR_ALIGN;
+  if (M == 0) return SPLR_OK;
+  const size_t need = experts_workspace_bytes(M, r);
+  if (need > 0 && (!workspace || ws_bytes < need)) return SPLR_ERR_WORKSPACE;
+  if (need > 0 && !aligned16(workspace)) return SPLR_ERR_ALIGN;
+  return from_hip(splr::launch_fused(X, M, n_in, offsets, n_experts, values, meta, n_out, U, V, r,
+                                     dtype == SPLR_BF16, ep, Y, y_dtype == SPLR_BF16, workspace, stream));
+}
+
+}  // extern "C"
+
 // ---------------------------------------------------------------- splr_linear_noalloc
 // For callers that cannot allocate: the first-stage workspace lives in a file-scope device array.
 // Each GPU the library runs on holds its own copy (from the first call on it until the process

@@ -5,6 +5,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "epilogue.hpp"
+
 namespace splr {
 
 // Dispatch limits of one launch (HIP on gfx9): fewer than 2^32 work-items along x, at most 65535
@@ -72,6 +74,14 @@ hipError_t launch_linear_decode(const void* X, int64_t M, int64_t n_in, const vo
 hipError_t launch_linear_f32(const float* X, int64_t M, int64_t n_in, const float* values, const uint32_t* meta,
                              int64_t n_out, const float* U, int64_t r, const float* T, void* Y, bool y_bf16,
                              hipStream_t stream);
+
+// The layer product with a fused epilogue (splr_linear_fused: offsets NULL, one expert; and
+// splr_linear_experts), both stages. The workspace holds T (fused_workspace_bytes).
+size_t fused_workspace_bytes(int64_t M, int64_t r);
+hipError_t launch_fused(const void* X, int64_t M, int64_t n_in, const int32_t* offsets, int64_t experts,
+                        const void* values, const uint32_t* meta, int64_t n_out, const void* U, const void* V,
+                        int64_t r, bool bf16, const Epilogue& ep, void* Y, bool y_bf16, void* workspace,
+                        hipStream_t stream);
 
 hipError_t launch_dense_reconstruct(const void* values, const uint32_t* meta, const void* U, const void* V,
                                     int64_t n_out, int64_t n_in, int64_t r, bool bf16, float* W_hat,
