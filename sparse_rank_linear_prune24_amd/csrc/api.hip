@@ -303,9 +303,15 @@ splr_status_t check_epilogue(const splr_epilogue_t* epilogue, splr_dtype_t dtype
   return SPLR_OK;
 }
 
-size_t experts_workspace_bytes(int64_t M, int64_t r) {
-  return r == 0 ? 0 : round_up(splr::fused_workspace_bytes(M, r), 256);
+splr::FusedCall fused_call(const void* X, int64_t M, int64_t n_in, const int32_t* offsets, int64_t experts,
+                           const void* values, const uint32_t* meta, int64_t n_out, const void* U, const void* V,
+                           int64_t r, splr_dtype_t dtype, const splr::Epilogue& ep, void* Y, splr_dtype_t y_dtype,
+                           void* workspace) {
+  return splr::FusedCall{X, M, n_in, offsets, experts, values, meta, n_out, U, V, r, dtype == SPLR_BF16, ep, Y,
+                         y_dtype == SPLR_BF16, workspace, 1};
 }
+
+size_t experts_workspace_bytes(const splr::FusedCall& c) { return round_up(splr::fused_workspace_bytes(c), 256); }
 
 }  // namespace
 
@@ -320,17 +326,20 @@ splr_status_t splr_linear_fused(const void* X, int64_t M, int64_t n_in, const vo
   splr::Epilogue ep;
   s = check_epilogue(epilogue, dtype, y_dtype, &ep);
   if (s != SPLR_OK) return s;
-  return from_hip(splr::launch_fused(X, M, n_in, nullptr, 1, values, meta, n_out, U, V, r, dtype == SPLR_BF16, ep, Y,
-                                     y_dtype == SPLR_BF16, workspace, stream));
+  const splr::FusedCall c =
+      fused_call(X, M, n_in, nullptr, 1, values, meta, n_out, U, V, r, dtype, ep, Y, y_dtype, workspace);
+  if (!splr::fused_grids_fit(c)) return SPLR_ERR_SHAPE;
+  return from_hip(splr::launch_fused(c, stream));
 }
 
 size_t splr_linear_experts_workspace_bytes(int64_t M, int64_t n_experts, int64_t n_out, int64_t n_in, int64_t r,
                                            splr_dtype_t dtype) {
-  (void)n_out;
   if (M < 0 || M > kMaxRows || n_experts < 1 || n_experts > SPLR_EXPERTS_MAX || check_in(n_in) != SPLR_OK ||
       check_rank(r) != SPLR_OK || !dtype_ok(dtype))
     return 0;
-  return experts_workspace_bytes(M, r);
+  const int32_t any = 0;  // a non-null `offsets`: a call by expert
+  return experts_workspace_bytes(fused_call(nullptr, M, n_in, &any, n_experts, nullptr, nullptr, n_out, nullptr,
+                                            nullptr, r, dtype, splr::Epilogue{}, nullptr, SPLR_FP32, nullptr));
 }
 
 splr_status_t splr_linear_experts(const void* X, int64_t M, int64_t n_in, const int32_t* offsets, int64_t n_experts,
@@ -356,11 +365,13 @@ splr_status_t splr_linear_experts(const void* X, int64_t M, int64_t n_in, const 
       (reinterpret_cast<uintptr_t>(offsets) & 3u) || (r > 0 && (!aligned16(U) || !aligned16(V))))
     return SPLR_ERR_ALIGN;
   if (M == 0) return SPLR_OK;
-  const size_t need = experts_workspace_bytes(M, r);
+  const splr::FusedCall c =
+      fused_call(X, M, n_in, offsets, n_experts, values, meta, n_out, U, V, r, dtype, ep, Y, y_dtype, workspace);
+  if (!splr::fused_grids_fit(c)) return SPLR_ERR_SHAPE;
+  const size_t need = experts_workspace_bytes(c);
   if (need > 0 && (!workspace || ws_bytes < need)) return SPLR_ERR_WORKSPACE;
   if (need > 0 && !aligned16(workspace)) return SPLR_ERR_ALIGN;
-  return from_hip(splr::launch_fused(X, M, n_in, offsets, n_experts, values, meta, n_out, U, V, r,
-                                     dtype == SPLR_BF16, ep, Y, y_dtype == SPLR_BF16, workspace, stream));
+  return from_hip(splr::launch_fused(c, stream));
 }
 
 }  // extern "C"

@@ -4,6 +4,8 @@
 // combine their partial accumulators through LDS in a fixed order; wave 0 adds the rank-r term and
 // stores Y.
 #include "common.hpp"
+#include "epilogue.hpp"
+#include "groups.hpp"
 #include "kernels.hpp"
 #include "tile_common.hpp"
 
@@ -29,11 +31,31 @@ struct URow {
   __device__ __forceinline__ bf16x8_t pair23() const { return as_bf16x8(u32x4_t{d0[1], d0[3], d1[1], d1[3]}); }
 };
 
-template <int MB, int P, int WAVES>
+// MODE: the plain product, with the fused epilogue, or that for rows grouped by expert (blockIdx.y is
+// then a token block among all experts', and the operands are shifted to the block's expert and rows)
+constexpr int kModePlain = 0, kModeFused = 1, kModeExperts = 2;
+
+template <int MB, int P, int WAVES, int MODE = kModePlain>
 __global__ __launch_bounds__(64 * WAVES) void linear_decode_kernel(
-    const uint16_t* __restrict__ X, const u32x4_t* __restrict__ values, const uint32_t* __restrict__ meta,
-    const uint16_t* __restrict__ U, const float* __restrict__ Tpart, int slices, void* __restrict__ Y, int y_bf16, int M, int K,
-    int n_out, int r) {
+    const uint16_t* __restrict__ X_, const u32x4_t* __restrict__ values_, const uint32_t* __restrict__ meta_,
+    const uint16_t* __restrict__ U_, const float* __restrict__ Tpart_, int slices, void* Y, int y_bf16, int M, int K,
+    int n_out, int r, Epilogue ep, Groups groups) {
+  int first_row = 0, m_block = blockIdx.y;
+  size_t e = 0;
+  if constexpr (MODE == kModeExperts) {
+    const GroupTile gt = find_group_tile<16 * MB>(groups, blockIdx.y);
+    if (gt.expert < 0) return;
+    first_row = gt.lo;
+    m_block = blockIdx.y - gt.first;
+    M = gt.rows;
+    e = gt.expert;
+  }
+  const size_t e_tiles = e * ((n_out + 15) / 16);  // tile rows before this expert's
+  const uint16_t* __restrict__ X = X_ + (size_t)first_row * K;
+  const u32x4_t* __restrict__ values = values_ + e_tiles * ((K + 63) / 64) * 64;
+  const uint32_t* __restrict__ meta = meta_ + e_tiles * meta_blocks((K + 63) / 64) * 256;
+  const uint16_t* __restrict__ U = U_ + e * n_out * r;
+  const float* __restrict__ Tpart = Tpart_ + (size_t)first_row * r;
   constexpr int kXLoads = 2 * MB;  // 8 tokens x 128 bytes per load instruction, 16*MB tokens
   __shared__ u32x4_t xs[WAVES][16 * MB * kXPitchU4];
   __shared__ f32x4_t red[(WAVES - 1) * MB * 64];
@@ -42,7 +64,7 @@ __global__ __launch_bounds__(64 * WAVES) void linear_decode_kernel(
   // loop control instead of exec-mask loops)
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int sub = lane & 15, quad = lane >> 4;
-  const int tr = blockIdx.x, m0 = blockIdx.y * 16 * MB;
+  const int tr = blockIdx.x, m0 = m_block * 16 * MB;
   const int TK = (K + 63) / 64;
 
   const u32x4_t* vsrc = values + (size_t)tr * TK * 64 + lane;
@@ -87,8 +109,24 @@ __global__ __launch_bounds__(64 * WAVES) void linear_decode_kernel(
   const bool t_pre = r <= 64 * kPreRankBlocks;
   TPairBuilder<16 * MB, 64 * WAVES, MB == 1 ? 8 : 0> tb;  // 16 tokens: at most 8 K slices, all in one round
   if (t_pre && r > 0) {
-    tb.init(Tpart, slices, M, r, m0, 0, threadIdx.x);
+    tb.init(Tpart, slices, M, r, m0, 0, threadIdx.x, MODE == kModeExperts ? groups.rows : 0);
     tb.issue(0);
+  }
+  // the epilogue's operands for the entries that wave 0 stores, loaded ahead like U's fragments: rows
+  // n .. n+3 of token m0 + 16 j + lane % 16
+  f32x4_t bias = {0, 0, 0, 0}, gate[MB], residual[MB];
+  if constexpr (MODE != kModePlain) {
+    if (wave == 0) {
+      const int n = tr * 16 + 4 * quad, left = n_out - n;
+      const bool vec = (n_out & 3) == 0 && left >= 4;
+      if (ep.bias) bias = load4(ep.bias, e * n_out + n, ep.bias_bf16, vec, left);
+#pragma unroll
+      for (int j = 0; j < MB; ++j) {
+        const size_t at = (size_t)(first_row + min(m0 + 16 * j + sub, M - 1)) * n_out + n;
+        if (ep.gate) gate[j] = load4(ep.gate, at, y_bf16, vec, left);
+        if (ep.residual) residual[j] = load4(ep.residual, at, y_bf16, vec, left);
+      }
+    }
   }
   // U's fragments for wave 0's rank-r term, loaded now: after the loop their memory latency would
   // be exposed at the end of the call
@@ -155,13 +193,27 @@ __global__ __launch_bounds__(64 * WAVES) void linear_decode_kernel(
     }
   } else {
     for (int j0 = 0; j0 < r; j0 += 64) {
-      build_t_pair<16 * MB, 64 * WAVES>(Tpart, slices, M, r, m0, j0, xs[0], xs[1], threadIdx.x);
+      build_t_pair<16 * MB, 64 * WAVES>(Tpart, slices, M, r, m0, j0, xs[0], xs[1], threadIdx.x,
+                                        MODE == kModeExperts ? groups.rows : 0);
       lds_barrier();
       if (wave == 0) lowrank_block<1, MB>(acc, U, xs[0], xs[1], n_out, r, j0, tr * 16, lane);
       lds_barrier();
     }
   }
-  if (wave == 0) store_tile<1, MB>(acc, Y, y_bf16, M, n_out, tr * 16, m0, lane);
+  if (wave != 0) return;
+  if constexpr (MODE == kModePlain) {
+    store_tile<1, MB>(acc, Y, y_bf16, M, n_out, tr * 16, m0, lane);
+  } else {
+    const int n = tr * 16 + 4 * quad, left = n_out - n;
+    const bool vec = (n_out & 3) == 0 && left >= 4;
+#pragma unroll
+    for (int j = 0; j < MB; ++j) {
+      const int m = m0 + 16 * j + sub;
+      if (m >= M) continue;
+      const f32x4_t y = finish4(acc[0][j], bias, ep, gate[j], residual[j]);
+      store4<false>(Y, (size_t)(first_row + m) * n_out + n, y_bf16, vec, left, y);
+    }
+  }
 }
 
 dim3 decode_grid(int64_t M, int64_t n_out, int MB) {
@@ -176,7 +228,24 @@ hipError_t launch_decode(const void* X, int64_t M, int64_t n_in, const void* val
   const dim3 grid = decode_grid(M, n_out, MB);
   linear_decode_kernel<MB, P, W><<<grid, dim3(64 * W), 0, stream>>>(
       (const uint16_t*)X, (const u32x4_t*)values, meta, (const uint16_t*)U, Tpart, slices, Y, y_bf16, (int)M,
-      (int)n_in, (int)n_out, (int)r);
+      (int)n_in, (int)n_out, (int)r, Epilogue{}, Groups{});
+  return hipGetLastError();
+}
+
+template <int MB>
+hipError_t launch_fused_mb(const FusedCall& c, hipStream_t stream) {
+  constexpr int P = MB == 1 ? 8 : 4, W = 4;
+  const bool experts = c.offsets != nullptr;
+  const dim3 grid((unsigned)ceil_div(c.n_out, 16),
+                  (unsigned)(experts ? most_group_tiles(c.M, c.experts, 16 * MB) : ceil_div(c.M, 16 * MB)));
+  const auto launch = [&](auto kernel) {
+    kernel<<<grid, dim3(64 * W), 0, stream>>>((const uint16_t*)c.X, (const u32x4_t*)c.values, c.meta,
+                                              (const uint16_t*)c.U, (const float*)c.workspace, c.slices, c.Y,
+                                              c.y_bf16 ? 1 : 0, (int)c.M, (int)c.n_in, (int)c.n_out, (int)c.r, c.ep,
+                                              Groups{c.offsets, (int)c.experts, (int)c.M});
+  };
+  if (experts) launch(linear_decode_kernel<MB, P, W, kModeExperts>);
+  else launch(linear_decode_kernel<MB, P, W, kModeFused>);
   return hipGetLastError();
 }
 
@@ -193,6 +262,12 @@ hipError_t launch_linear_decode(const void* X, int64_t M, int64_t n_in, const vo
   if (M <= 16) return launch_decode<1>(X, M, n_in, values, meta, n_out, U, r, Tpart, slices, Y, yb, stream);
   if (M <= 32) return launch_decode<2>(X, M, n_in, values, meta, n_out, U, r, Tpart, slices, Y, yb, stream);
   return launch_decode<4>(X, M, n_in, values, meta, n_out, U, r, Tpart, slices, Y, yb, stream);
+}
+
+hipError_t launch_fused_decode(const FusedCall& c, int tokens, hipStream_t stream) {
+  if (tokens <= 16) return launch_fused_mb<1>(c, stream);
+  if (tokens <= 32) return launch_fused_mb<2>(c, stream);
+  return launch_fused_mb<4>(c, stream);
 }
 
 }  // namespace splr

@@ -1,10 +1,13 @@
 // The layer product with a fused epilogue, for one layer or for rows grouped by expert:
 //   Z = X S^T + (X V^T) U^T + bias,  Y = act(Z) * gate + residual     (LoSparse page, section 3.2).
-// One lane per output, for every type and size; a row's expert follows from the offsets.
+// Here: which kernels take a call, and the float32 kernels (one lane per output; a row's expert follows
+// from the offsets). The bfloat16 kernels are those of the plain product with the epilogue in their
+// last step (decode.hip, linear_bf16.hip).
 #include <algorithm>
 
 #include "common.hpp"
 #include "epilogue.hpp"
+#include "groups.hpp"
 #include "kernels.hpp"
 
 namespace splr {
@@ -25,8 +28,7 @@ __device__ __forceinline__ int expert_of_row(const int32_t* __restrict__ offsets
 }
 
 // T[m][j] = X[m] . V_e[j], one wave per output
-template <bool BF16>
-__global__ __launch_bounds__(256) void rows_lowrank_kernel(const void* __restrict__ X, const void* __restrict__ V,
+__global__ __launch_bounds__(256) void rows_lowrank_kernel(const float* __restrict__ X, const float* __restrict__ V,
                                                            const int32_t* __restrict__ offsets, int experts, int M,
                                                            int K, int r, float* __restrict__ T) {
   const int lane = threadIdx.x & 63;
@@ -35,19 +37,20 @@ __global__ __launch_bounds__(256) void rows_lowrank_kernel(const void* __restric
     const int64_t m = o / r, j = o - m * r;
     const int e = expert_of_row(offsets, experts, (int)m);
     if (e < 0) continue;
+    const float* x = X + (size_t)m * K;
+    const float* v = V + ((size_t)e * r + j) * K;
     float t = 0.0f;
-    for (int k = lane; k < K; k += 64)
-      t = fmaf(load_as_float(X, (size_t)m * K + k, BF16), load_as_float(V, ((size_t)e * r + j) * K + k, BF16), t);
+    for (int k = lane; k < K; k += 64) t = fmaf(x[k], v[k], t);
 #pragma unroll
     for (int off = 32; off > 0; off >>= 1) t += __shfl_xor(t, off);
     if (lane == 0) T[o] = t;
   }
 }
 
-template <bool BF16>
-__global__ __launch_bounds__(256) void rows_fused_kernel(const void* __restrict__ X, const void* __restrict__ values,
+__global__ __launch_bounds__(256) void rows_fused_kernel(const float* __restrict__ X,
+                                                         const float* __restrict__ values,
                                                          const uint32_t* __restrict__ meta,
-                                                         const void* __restrict__ U, const float* __restrict__ T,
+                                                         const float* __restrict__ U, const float* __restrict__ T,
                                                          const int32_t* __restrict__ offsets, int experts,
                                                          Epilogue ep, void* Y, int y_bf16, int M, int K, int n_out,
                                                          int r) {
@@ -60,27 +63,25 @@ __global__ __launch_bounds__(256) void rows_fused_kernel(const void* __restrict_
     const int e = expert_of_row(offsets, experts, m);
     if (e < 0) continue;
     const int64_t tr = (int64_t)e * TR + n / 16;
+    const float* x = X + (size_t)m * K;
     float acc = 0.0f;
 #pragma unroll 8
     for (int grp = 0; grp < K / 4; ++grp) {
       const int tk = grp / 16, gi = grp % 16, slot = n % 16 + 16 * (gi / 4);
       const uint32_t nib = (meta_unit(meta, TKB, tr, tk, slot) >> (4 * (gi % 4))) & 0xFu;
-      const size_t kept = ((size_t)tr * TK + tk) * 512 + slot * 8 + 2 * (gi % 4);
-      const size_t x = (size_t)m * K + 4 * grp;
-      acc = fmaf(load_as_float(X, x + (nib & 3u), BF16), load_as_float(values, kept, BF16), acc);
-      acc = fmaf(load_as_float(X, x + (nib >> 2), BF16), load_as_float(values, kept + 1, BF16), acc);
+      const float* kept = values + ((size_t)tr * TK + tk) * 512 + slot * 8 + 2 * (gi % 4);
+      acc = fmaf(x[4 * grp + (nib & 3u)], kept[0], acc);
+      acc = fmaf(x[4 * grp + (nib >> 2)], kept[1], acc);
     }
     float lr = 0.0f;
-    for (int j = 0; j < r; ++j)
-      lr = fmaf(T[(size_t)m * r + j], load_as_float(U, ((size_t)e * n_out + n) * r + j, BF16), lr);
+    for (int j = 0; j < r; ++j) lr = fmaf(T[(size_t)m * r + j], U[((size_t)e * n_out + n) * r + j], lr);
     const size_t o = (size_t)m * n_out + n;
-    float y = acc + lr;
-    if (ep.bias) y += load_as_float(ep.bias, (size_t)e * n_out + n, BF16);
-    y = activate(y, ep.act);
-    if (ep.gate) y *= load_as_float(ep.gate, o, y_bf16);
-    if (ep.residual) y += load_as_float(ep.residual, o, y_bf16);
-    if (y_bf16) ((uint16_t*)Y)[o] = (uint16_t)float_to_bf16_bits(y);
-    else ((float*)Y)[o] = y;
+    const f32x4_t zero = {0, 0, 0, 0};
+    const f32x4_t bias = ep.bias ? load4(ep.bias, (size_t)e * n_out + n, false, false, 1) : zero;
+    const f32x4_t gate = ep.gate ? load4(ep.gate, o, y_bf16, false, 1) : zero;
+    const f32x4_t residual = ep.residual ? load4(ep.residual, o, y_bf16, false, 1) : zero;
+    const f32x4_t y = finish4(f32x4_t{acc + lr, 0, 0, 0}, bias, ep, gate, residual);
+    store4<false>(Y, o, y_bf16, false, 1, y);
   }
 }
 
@@ -88,24 +89,65 @@ constexpr int64_t kMaxBlocks = int64_t(1) << 20;
 
 }  // namespace
 
-size_t fused_workspace_bytes(int64_t M, int64_t r) { return (size_t)M * r * sizeof(float); }
+namespace {
 
-hipError_t launch_fused(const void* X, int64_t M, int64_t n_in, const int32_t* offsets, int64_t experts,
-                        const void* values, const uint32_t* meta, int64_t n_out, const void* U, const void* V,
-                        int64_t r, bool bf16, const Epilogue& ep, void* Y, bool y_bf16, void* workspace,
-                        hipStream_t stream) {
-  float* T = (float*)workspace;
-  if (r > 0) {
-    const dim3 grid((unsigned)std::min(ceil_div(M * r, 4), kMaxBlocks));
-    const auto stage1 = bf16 ? rows_lowrank_kernel<true> : rows_lowrank_kernel<false>;
-    stage1<<<grid, dim3(256), 0, stream>>>(X, V, offsets, (int)experts, (int)M, (int)n_in, (int)r, T);
+// Tokens that the decode kernel takes together, 0 where the prefill kernel is faster; for experts by the
+// rows an expert has on average.
+int decode_tokens(const FusedCall& c) {
+  if (!c.offsets) return c.M <= kDecodeMaxTokens ? (int)c.M : 0;
+  const int64_t mean = ceil_div(c.M, c.experts);
+  if (mean <= 12) return 16;
+  if (mean <= 24) return 32;
+  return mean <= 64 ? 64 : 0;
+}
+
+dim3 rows_grid(const FusedCall& c) {
+  return dim3((unsigned)std::min(ceil_div(c.n_out, 64) * ceil_div(c.M, 4), kMaxBlocks));
+}
+
+int slices_of(const FusedCall& c) {
+  if (!c.bf16 || c.r == 0) return 1;
+  return c.offsets ? experts_lowrank_slices(c) : lowrank_slices(c.M, c.n_in, c.r, true);
+}
+
+}  // namespace
+
+size_t fused_workspace_bytes(const FusedCall& c) {
+  return c.M == 0 || c.r == 0 ? 0 : (size_t)slices_of(c) * c.M * c.r * sizeof(float);
+}
+
+bool fused_grids_fit(const FusedCall& c) {
+  if (!c.bf16) return true;  // both grids are capped
+  if (c.r > 0 && !(c.offsets ? experts_lowrank_grid_fits(c) : lowrank_grids_fit(c.M, c.n_in, c.r, true))) return false;
+  const int tokens = decode_tokens(c);
+  if (!tokens) return fused_prefill_grid_fits(c);
+  const int64_t block = tokens <= 16 ? 16 : tokens <= 32 ? 32 : 64;
+  return (c.offsets ? most_group_tiles(c.M, c.experts, block) : ceil_div(c.M, block)) <= 65535 &&
+         grid_fits(dim3((unsigned)ceil_div(c.n_out, 16)), 256);
+}
+
+hipError_t launch_fused(FusedCall c, hipStream_t stream) {
+  c.slices = slices_of(c);
+  if (c.bf16) {
+    if (c.r > 0) {
+      const hipError_t e = c.offsets ? launch_experts_lowrank(c, stream)
+                                     : launch_lowrank(c.X, c.V, c.M, c.n_in, c.r, true, c.workspace, stream);
+      if (e != hipSuccess) return e;
+    }
+    const int tokens = decode_tokens(c);
+    return tokens ? launch_fused_decode(c, tokens, stream) : launch_fused_prefill(c, stream);
+  }
+  float* T = (float*)c.workspace;
+  if (c.r > 0) {
+    const dim3 grid((unsigned)std::min(ceil_div(c.M * c.r, 4), kMaxBlocks));
+    rows_lowrank_kernel<<<grid, dim3(256), 0, stream>>>((const float*)c.X, (const float*)c.V, c.offsets,
+                                                        (int)c.experts, (int)c.M, (int)c.n_in, (int)c.r, T);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  const dim3 grid((unsigned)std::min(ceil_div(n_out, 64) * ceil_div(M, 4), kMaxBlocks));
-  const auto stage2 = bf16 ? rows_fused_kernel<true> : rows_fused_kernel<false>;
-  stage2<<<grid, dim3(256), 0, stream>>>(X, values, meta, U, T, offsets, (int)experts, ep, Y, y_bf16 ? 1 : 0, (int)M,
-                                         (int)n_in, (int)n_out, (int)r);
+  rows_fused_kernel<<<rows_grid(c), dim3(256), 0, stream>>>(
+      (const float*)c.X, (const float*)c.values, c.meta, (const float*)c.U, T, c.offsets, (int)c.experts, c.ep, c.Y,
+      c.y_bf16 ? 1 : 0, (int)c.M, (int)c.n_in, (int)c.n_out, (int)c.r);
   return hipGetLastError();
 }
 

@@ -75,13 +75,38 @@ hipError_t launch_linear_f32(const float* X, int64_t M, int64_t n_in, const floa
                              int64_t n_out, const float* U, int64_t r, const float* T, void* Y, bool y_bf16,
                              hipStream_t stream);
 
-// The layer product with a fused epilogue (splr_linear_fused: offsets NULL, one expert; and
-// splr_linear_experts), both stages. The workspace holds T (fused_workspace_bytes).
-size_t fused_workspace_bytes(int64_t M, int64_t r);
-hipError_t launch_fused(const void* X, int64_t M, int64_t n_in, const int32_t* offsets, int64_t experts,
-                        const void* values, const uint32_t* meta, int64_t n_out, const void* U, const void* V,
-                        int64_t r, bool bf16, const Epilogue& ep, void* Y, bool y_bf16, void* workspace,
-                        hipStream_t stream);
+// The layer product with a fused epilogue: splr_linear_fused (offsets NULL, one expert) and
+// splr_linear_experts. A call's operands, as its launchers take them.
+struct FusedCall {
+  const void* X;
+  int64_t M, n_in;
+  const int32_t* offsets;
+  int64_t experts;
+  const void* values;
+  const uint32_t* meta;
+  int64_t n_out;
+  const void* U;
+  const void* V;
+  int64_t r;
+  bool bf16;
+  Epilogue ep;
+  void* Y;
+  bool y_bf16;
+  void* workspace;  // T (fused_workspace_bytes)
+  int slices;       // K slices of T, set by launch_fused
+};
+size_t fused_workspace_bytes(const FusedCall& c);
+// Whether every launch of the call fits the dispatch limits.
+bool fused_grids_fit(const FusedCall& c);
+hipError_t launch_fused(FusedCall c, hipStream_t stream);
+// Its parts. Stage 1 of the experts in bfloat16 and its K slices; stage 2 for many tokens a group
+// (prefill) and for few (decode, with the tokens a workgroup takes together).
+int experts_lowrank_slices(const FusedCall& c);
+hipError_t launch_experts_lowrank(const FusedCall& c, hipStream_t stream);
+hipError_t launch_fused_prefill(const FusedCall& c, hipStream_t stream);
+hipError_t launch_fused_decode(const FusedCall& c, int tokens, hipStream_t stream);
+bool fused_prefill_grid_fits(const FusedCall& c);
+bool experts_lowrank_grid_fits(const FusedCall& c);
 
 hipError_t launch_dense_reconstruct(const void* values, const uint32_t* meta, const void* U, const void* V,
                                     int64_t n_out, int64_t n_in, int64_t r, bool bf16, float* W_hat,

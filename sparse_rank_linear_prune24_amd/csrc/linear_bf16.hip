@@ -26,7 +26,11 @@
 // -> registers (raw buffer loads); X is shared through a five-slot LDS ring; workgroups are
 // remapped so the tiles that one XCD (own L2) runs share X and S. Its DENSE form expands S to
 // dense bfloat16 in registers and runs dense MFMAs instead (the measured alternative).
+#include <algorithm>
+
 #include "common.hpp"
+#include "epilogue.hpp"
+#include "groups.hpp"
 #include "kernels.hpp"
 #include "tile_common.hpp"
 
@@ -91,6 +95,56 @@ __device__ __forceinline__ void store_tile_rows_lds(const f32x4_t (&acc)[NI][NJ]
           for (int e = 0; e < 4; ++e)
             if (n + e < n_out) yrow[n + e] = v[e];
         }
+      }
+    }
+  }
+}
+
+// store_tile_rows_lds with the fused epilogue between the LDS buffer and Y: each lane finishes four
+// consecutive entries of a token row, with gate and residual read (and Y written) as whole rows. The
+// rounds over 32-token slices run as a loop, not unrolled, so that the activations' code exists once
+// (straight-line it would exceed the instruction cache); only the reads of the accumulators, which need
+// constant indexes, are per round. `row0` is the first token of the tile in Y, gate and residual.
+template <int NI, int NJ, bool NT>
+__device__ __forceinline__ void store_tile_rows_fused(const f32x4_t (&acc)[NI][NJ], float* buf, const Epilogue& ep,
+                                                      size_t bias_row, void* Y, int y_bf16, int M, int n_out,
+                                                      int nrow0, int m0, size_t row0, int lane) {
+  constexpr int R = 16 * NI, kPitch = R + 4, kTok = 32;
+  constexpr int kLanesPerTok = R / 4, kTokPerRead = 64 / kLanesPerTok, kBatch = 4;
+  static_assert(NJ % 2 == 0 && kTok % (kBatch * kTokPerRead) == 0, "32 tokens a round");
+  const int q = lane >> 4, sb = lane & 15;
+  const int rl = lane % kLanesPerTok, tl = lane / kLanesPerTok;
+  const int n = nrow0 + 4 * rl, left = n_out - n;
+  const bool vec = (n_out & 3) == 0 && left >= 4;
+  f32x4_t bias = {0, 0, 0, 0};
+  if (ep.bias && left > 0) bias = load4(ep.bias, bias_row + n, ep.bias_bf16, vec, left);
+#pragma unroll 1
+  for (int c = 0; c < NJ / 2; ++c) {
+    static_for<NJ / 2>([&](auto cc) {
+      if (c == decltype(cc)::value) {
+#pragma unroll
+        for (int jj = 0; jj < 2; ++jj)
+#pragma unroll
+          for (int i = 0; i < NI; ++i)
+            *(f32x4_t*)(buf + (16 * jj + sb) * kPitch + 16 * i + 4 * q) = acc[i][2 * decltype(cc)::value + jj];
+      }
+    });
+    if (m0 + 32 * c >= M) break;
+#pragma unroll 1
+    for (int k = 0; k < kTok / kTokPerRead; k += kBatch) {
+      f32x4_t gate[kBatch], residual[kBatch];
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {  // tokens past the last one read it again
+        const int t = min(32 * c + (k + b) * kTokPerRead + tl, M - 1 - m0);
+        const size_t at = (row0 + t) * n_out + n;
+        if (ep.gate && left > 0) gate[b] = load4(ep.gate, at, y_bf16, vec, left);
+        if (ep.residual && left > 0) residual[b] = load4(ep.residual, at, y_bf16, vec, left);
+      }
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        const int t = (k + b) * kTokPerRead + tl;
+        const f32x4_t y = finish4(*(const f32x4_t*)(buf + t * kPitch + 4 * rl), bias, ep, gate[b], residual[b]);
+        if (m0 + 32 * c + t < M && left > 0) store4<NT>(Y, (row0 + 32 * c + t) * n_out + n, y_bf16, vec, left, y);
       }
     }
   }
@@ -265,10 +319,16 @@ __device__ __forceinline__ T pick_layer(const T (&a)[kMaxGroup], int layer) {
 // groups ahead of its NI MFMAs; X goes through a five-slot LDS ring with a barrier every second
 // step. The first two 64-rank blocks of the rank-r term run before the main loop (their T pairs in
 // four of the ring's slots); further blocks after it.
-template <int NI, int LA, int P, int EPI, int WAVES = 8, bool DENSE = false>
+// MODE: the plain product, with the fused epilogue, or that for rows grouped by expert: the tiles are
+// then those of every expert's own rows, expert after expert, and the operands are shifted to the
+// expert of the tile (lg holds the first expert's, `layers` is 1).
+constexpr int kModePlain = 0, kModeFused = 1, kModeExperts = 2;
+
+template <int NI, int LA, int P, int EPI, int WAVES = 8, bool DENSE = false, int MODE = kModePlain>
 __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(WAVES / 4, WAVES / 4))) void
 linear_prefill_wide_kernel(const LayerGroup lg, int layers, int slices, int y_bf16, int M, int K, int n_out, int r,
-                           int tiles_n, int tiles_m, int tiles_per_xcd, int group_m) {
+                           int tiles_n, int tiles_m, int tiles_per_xcd, int group_m, const Epilogue ep,
+                           const Groups groups) {
   constexpr int NJ = 8, PX = 2;
   static_assert(WAVES == 4 || WAVES == 8, "one or two waves per SIMD");
   constexpr int BN = 16 * NI * WAVES;  // 512 or 256 rows
@@ -291,17 +351,28 @@ linear_prefill_wide_kernel(const LayerGroup lg, int layers, int slices, int y_bf
 
   // XCD-aware tile order: each XCD (own L2) runs a contiguous range of the tiles, layer after layer
   const int b = blockIdx.x;
+  GroupTile gt = {0, 0, M, 0, tiles_m};
+  if constexpr (MODE == kModeExperts) tiles_per_xcd = (group_tiles_total<BM>(groups) * tiles_n + 7) / 8;
+  if (MODE == kModeExperts && (b >> 3) >= tiles_per_xcd) return;
   const int logical_all = (b & 7) * tiles_per_xcd + (b >> 3);
+  if constexpr (MODE == kModeExperts) {
+    gt = find_group_tile<BM>(groups, logical_all / tiles_n);
+    if (gt.expert < 0) return;
+    tiles_m = gt.tiles;
+    M = gt.rows;
+  }
   const int per_layer = tiles_n * tiles_m;
-  if (logical_all >= per_layer * layers) return;
-  const int layer = logical_all / per_layer;
-  const int logical = logical_all - layer * per_layer;
-  const uint16_t* __restrict__ X = pick_layer(lg.X, layer);
-  const u32x4_t* __restrict__ values = pick_layer(lg.values, layer);
-  const uint32_t* __restrict__ meta = pick_layer(lg.meta, layer);
-  const uint16_t* __restrict__ U = pick_layer(lg.U, layer);
-  const float* __restrict__ Tpart = pick_layer(lg.Tpart, layer);
-  void* __restrict__ Y = pick_layer(lg.Y, layer);
+  if (MODE != kModeExperts && logical_all >= per_layer * layers) return;
+  const int layer = MODE == kModeExperts ? 0 : logical_all / per_layer;
+  const int logical = logical_all - (MODE == kModeExperts ? gt.first * tiles_n : layer * per_layer);
+  const size_t e = gt.expert, first_row = gt.lo, e_tiles = e * ((n_out + 15) / 16);
+  const uint16_t* __restrict__ X = pick_layer(lg.X, layer) + first_row * K;
+  const u32x4_t* __restrict__ values = pick_layer(lg.values, layer) + e_tiles * ((K + 63) / 64) * 64;
+  const uint32_t* __restrict__ meta = pick_layer(lg.meta, layer) + e_tiles * meta_blocks((K + 63) / 64) * 256;
+  const uint16_t* __restrict__ U = pick_layer(lg.U, layer) + e * n_out * r;
+  const float* __restrict__ Tpart = pick_layer(lg.Tpart, layer) + first_row * r;
+  void* Y = pick_layer(lg.Y, layer);
+  const int t_rows = MODE == kModeExperts ? groups.rows : 0;
   const int per_group = group_m * tiles_n;
   const int g = logical / per_group;
   const int first_m = g * group_m;
@@ -353,10 +424,15 @@ linear_prefill_wide_kernel(const LayerGroup lg, int layers, int slices, int y_bf
   const int x_end = x_rows * K * 2, v_end = rows_here * s_stride, m_end = rows_here * m_stride;
   auto load_x = [&](int kc, u32x4_t (&v)[kXLoads]) {
     // half tail step: re-read valid columns (S is zero there); per lane, as the chunk decides
-    const int back = (kc < TK && kc * 64 + 8 * xchunk >= K) ? 64 : 0;
+    // (with the fused epilogue: read zeros, so that an infinite X entry is not multiplied by S's zero)
+    const bool tail = kc < TK && kc * 64 + 8 * xchunk >= K;
+    const int back = tail ? 64 : 0;
     const int so = kc < TK ? kc * 128 : x_end;
 #pragma unroll
-    for (int t = 0; t < kXLoads; ++t) v[t] = __builtin_amdgcn_raw_buffer_load_b128(xrs, x_off[t] - back, so, 0);
+    for (int t = 0; t < kXLoads; ++t) {
+      const int xo = MODE == kModePlain ? x_off[t] - back : tail ? x_end : x_off[t];
+      v[t] = __builtin_amdgcn_raw_buffer_load_b128(xrs, xo, so, 0);
+    }
   };
   auto load_s_frag = [&](int kc, int i, u32x4_t& va) {
     va = __builtin_amdgcn_raw_buffer_load_b128(vrs, s_off, kc < TK ? i * s_stride + kc * 1024 : v_end, 0);
@@ -468,8 +544,8 @@ linear_prefill_wide_kernel(const LayerGroup lg, int layers, int slices, int y_bf
   if (r_pre > 0) {
     const bool two = r_pre > 64;  // wave-uniform: the second block's T pair is built only when used
     TPairBuilder<BM, 64 * WAVES, 2> tb0, tb1;
-    tb0.init(Tpart, slices, M, r, m0, 0, threadIdx.x);
-    tb1.init(Tpart, slices, M, r, m0, 64, threadIdx.x);  // ranks >= r read as zeros
+    tb0.init(Tpart, slices, M, r, m0, 0, threadIdx.x, t_rows);
+    tb1.init(Tpart, slices, M, r, m0, 64, threadIdx.x, t_rows);  // ranks >= r read as zeros
     tb0.issue(0);
     if (two) tb1.issue(0);
     __builtin_amdgcn_sched_barrier(0);
@@ -522,13 +598,19 @@ linear_prefill_wide_kernel(const LayerGroup lg, int layers, int slices, int y_bf
   for (int j0 = r_pre; j0 < r; j0 += 64) {
     UFragments<NI> uf;
     uf.load(U, n_out, r, j0, nrow0, lane);
-    build_t_pair<BM, 64 * WAVES>(Tpart, slices, M, r, m0, j0, xs, xs + kSlot, threadIdx.x);
+    build_t_pair<BM, 64 * WAVES>(Tpart, slices, M, r, m0, j0, xs, xs + kSlot, threadIdx.x, t_rows);
     lds_barrier();
     lowrank_block_acc<NI, NJ>(acc, uf, xs, xs + kSlot);
     lds_barrier();
   }
   accumulator_fence(acc);  // the last smfmac_acc results, before the stores
-  if constexpr ((EPI & kEpiRows) != 0) {
+  if constexpr (MODE != kModePlain) {
+    static_assert((EPI & kEpiRows) != 0 && WAVES * 32 * (16 * NI + 4) * 4 <= (int)sizeof(xs), "a private buffer per wave");
+    lds_barrier();
+    store_tile_rows_fused<NI, NJ, (EPI & kEpiDirectNT) != 0>(acc, (float*)xs + wave * 32 * (16 * NI + 4), ep,
+                                                            e * n_out, Y, y_bf16, M, n_out, nrow0, m0,
+                                                            first_row + m0, lane);
+  } else if constexpr ((EPI & kEpiRows) != 0) {
     static_assert(WAVES * 32 * (16 * NI + 4) * 4 <= (int)sizeof(xs), "a private buffer per wave");
     lds_barrier();  // every wave's reads of the ring are done before it is reused
     store_tile_rows_lds<NI, NJ, (EPI & kEpiDirectNT) != 0>(acc, (float*)xs + wave * 32 * (16 * NI + 4), Y, y_bf16, M,
@@ -607,7 +689,7 @@ hipError_t launch_linear_bf16_group(int layers, const void* const* X, int64_t M,
   // 512-row tiles, 8 % on the 256-row tiles)
   const auto launch = [&](auto kernel) {
     kernel<<<grid, dim3(512), 0, stream>>>(lg, layers, slices, yb, (int)M, (int)n_in, (int)n_out, (int)r, tiles_n,
-                                           tiles_m, per_xcd, group_m);
+                                           tiles_m, per_xcd, group_m, Epilogue{}, Groups{});
   };
   if (BN == 512) {
     if (y_nt)
@@ -641,7 +723,7 @@ hipError_t launch_linear_bf16_dense(const void* X, int64_t M, int64_t n_in, cons
   const LayerGroup lg = make_group(1, &X, &values, &meta, &U, &Tpart, &Y);
   const auto args = [&](auto kernel, int waves) {
     kernel<<<grid, dim3(64 * waves), 0, stream>>>(lg, 1, slices, 0, (int)M, (int)n_in, (int)n_out, (int)r, tiles_n,
-                                                  tiles_m, per_xcd, group_m);
+                                                  tiles_m, per_xcd, group_m, Epilogue{}, Groups{});
   };
   if (BN == 512) {
     if (y_nt)
@@ -651,6 +733,50 @@ hipError_t launch_linear_bf16_dense(const void* X, int64_t M, int64_t n_in, cons
   } else {
     args(linear_prefill_wide_kernel<2, 1, 2, kEpiRows, 8, true>, 8);
   }
+  return hipGetLastError();
+}
+
+namespace {
+// Tiles of a fused call: rows of a tile, and the grid. For experts the tiles are sized by how many the
+// rows make when every expert's last tile is half full; the grid holds the most that there can be.
+struct FusedTiles {
+  int bn, tiles_n, tiles_m;
+  dim3 grid;
+};
+FusedTiles fused_tiles(const FusedCall& c) {
+  FusedTiles t;
+  const int64_t likely = c.offsets ? ceil_div(c.M, 128) + std::min(c.experts, c.M) / 2 : ceil_div(c.M, 128);
+  t.bn = ceil_div(c.n_out, 512) * likely >= kWideMinTiles ? 512 : 256;
+  t.tiles_n = (int)ceil_div(c.n_out, t.bn);
+  t.tiles_m = (int)(c.offsets ? most_group_tiles(c.M, c.experts, 128) : ceil_div(c.M, 128));
+  t.grid = dim3((unsigned)(8 * ceil_div((int64_t)t.tiles_n * t.tiles_m, 8)));
+  return t;
+}
+}  // namespace
+
+bool fused_prefill_grid_fits(const FusedCall& c) {
+  const int64_t tiles = ceil_div(c.n_out, 256) * (c.offsets ? most_group_tiles(c.M, c.experts, 128) : ceil_div(c.M, 128));
+  return tiles < (int64_t(1) << 22) && grid_fits(fused_tiles(c).grid, 512);
+}
+
+hipError_t launch_fused_prefill(const FusedCall& c, hipStream_t stream) {
+  const FusedTiles t = fused_tiles(c);
+  const float* T = (const float*)c.workspace;
+  const LayerGroup lg = make_group(1, &c.X, &c.values, &c.meta, &c.U, &T, &c.Y);
+  const bool y_nt = (double)c.M * c.n_out * (c.y_bf16 ? 2 : 4) > kNonTemporalYBytes;
+  const auto launch = [&](auto kernel) {
+    kernel<<<t.grid, dim3(512), 0, stream>>>(lg, 1, c.slices, c.y_bf16 ? 1 : 0, (int)c.M, (int)c.n_in, (int)c.n_out,
+                                             (int)c.r, t.tiles_n, t.tiles_m, (int)t.grid.x / 8, 4, c.ep,
+                                             Groups{c.offsets, (int)c.experts, (int)c.M});
+  };
+  const auto rows = [&](auto mode) {
+    constexpr int kMode = decltype(mode)::value;
+    if (t.bn == 256) launch(linear_prefill_wide_kernel<2, 1, 2, kEpiRows, 8, false, kMode>);
+    else if (y_nt) launch(linear_prefill_wide_kernel<4, 1, 2, kEpiRowsNT, 8, false, kMode>);
+    else launch(linear_prefill_wide_kernel<4, 1, 2, kEpiRows, 8, false, kMode>);
+  };
+  if (c.offsets) rows(std::integral_constant<int, kModeExperts>{});
+  else rows(std::integral_constant<int, kModeFused>{});
   return hipGetLastError();
 }
 

@@ -14,6 +14,7 @@
 #include <utility>
 
 #include "common.hpp"
+#include "groups.hpp"
 #include "kernels.hpp"
 
 namespace splr {
@@ -35,11 +36,24 @@ __device__ __forceinline__ void static_for(F&& f) {
 
 // Grid (token blocks, rank blocks, K slices); slice z covers K steps [z*steps_per_slice, ...) and
 // writes the float32 partial sum part[z][m][j].
-template <int TF, int RF, int WAVES, int D>
+// EXPERTS: the token blocks are those of every expert's own rows, and X, V and part are shifted to the
+// block's expert (a slice of part still spans all experts' rows).
+template <int TF, int RF, int WAVES, int D, bool EXPERTS = false>
 __global__ __launch_bounds__(64 * WAVES) void lowrank_bf16_kernel(const uint16_t* __restrict__ X,
                                                                  const uint16_t* __restrict__ V, int M, int K,
                                                                  int r, int steps_per_slice,
-                                                                 float* __restrict__ part) {
+                                                                 float* __restrict__ part, Groups groups) {
+  int m_block = blockIdx.x;
+  const size_t slice_rows = M;
+  if constexpr (EXPERTS) {
+    const GroupTile gt = find_group_tile<16 * TF>(groups, blockIdx.x);
+    if (gt.expert < 0) return;
+    m_block -= gt.first;
+    M = gt.rows;
+    X += (size_t)gt.lo * K;
+    V += (size_t)gt.expert * r * K;
+    part += (size_t)gt.lo * r;
+  }
   constexpr int kRows = 16 * (TF + RF);  // staged rows per wave: X tokens, then V ranks
   constexpr int kLoads = kRows / 8;      // 8 rows x 128 bytes per load instruction
   __shared__ u32x4_t stage[WAVES][kRows * kPitchU4];
@@ -48,7 +62,7 @@ __global__ __launch_bounds__(64 * WAVES) void lowrank_bf16_kernel(const uint16_t
   // loop control instead of exec-mask loops)
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int sub = lane & 15, quad = lane >> 4;
-  const int m0 = blockIdx.x * 16 * TF, j0 = blockIdx.y * 16 * RF;
+  const int m0 = m_block * 16 * TF, j0 = blockIdx.y * 16 * RF;
   const int TK = (K + 63) / 64;
   const int kb = blockIdx.z * steps_per_slice, ke = min(TK, kb + steps_per_slice);
   const bool half_tail = (K & 63) != 0;  // the last step holds 32 valid columns
@@ -145,7 +159,7 @@ __global__ __launch_bounds__(64 * WAVES) void lowrank_bf16_kernel(const uint16_t
     for (int a = 0; a < RF; ++a)
 #pragma unroll
       for (int f = 0; f < TF; ++f) acc[a][f] += red[(((w - 1) * RF + a) * TF + f) * 64 + lane];
-  float* pz = part + (size_t)blockIdx.z * M * r;
+  float* pz = part + (size_t)blockIdx.z * slice_rows * r;
 #pragma unroll
   for (int a = 0; a < RF; ++a) {
     const int j = j0 + 16 * a + 4 * quad;
@@ -174,11 +188,11 @@ __device__ __forceinline__ void lds_barrier() {
 // straight from global memory into registers. Loads of both run P steps ahead in registers. V is
 // the A operand (two fixed 2:4 halves, as above), X the B operand. Rows past M and ranks past r
 // repeat the last valid row and are never stored.
-template <int TMW, int TRW, int WM, int WR, int P>
+template <int TMW, int TRW, int WM, int WR, int P, bool EXPERTS = false>
 __global__ __launch_bounds__(256) void lowrank_tile_kernel(const uint16_t* __restrict__ X,
                                                           const uint16_t* __restrict__ V, int M, int K, int r,
                                                           int rank_blocks, int steps_per_slice,
-                                                          float* __restrict__ part) {
+                                                          float* __restrict__ part, Groups groups) {
   static_assert(WM * WR == 4, "four waves");
   constexpr int BM = 16 * TMW * WM, BR = 16 * TRW * WR;
   constexpr int kChunks = BM * 8;                  // 16-byte chunks of X per step
@@ -187,8 +201,19 @@ __global__ __launch_bounds__(256) void lowrank_tile_kernel(const uint16_t* __res
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int sub = lane & 15, quad = lane >> 4;
   const int wm = wave % WM, wr = wave / WM;
-  const int mb = blockIdx.x / rank_blocks;
-  const int j0 = (blockIdx.x - mb * rank_blocks) * BR, m0 = mb * BM;
+  int mb = blockIdx.x / rank_blocks;
+  const int j0 = (blockIdx.x - mb * rank_blocks) * BR;
+  const size_t slice_rows = M;
+  if constexpr (EXPERTS) {  // as above
+    const GroupTile gt = find_group_tile<BM>(groups, mb);
+    if (gt.expert < 0) return;
+    mb -= gt.first;
+    M = gt.rows;
+    X += (size_t)gt.lo * K;
+    V += (size_t)gt.expert * r * K;
+    part += (size_t)gt.lo * r;
+  }
+  const int m0 = mb * BM;
   const int TK = (K + 63) / 64;
   const int kb = blockIdx.z * steps_per_slice;
   const int n_steps = min(TK, kb + steps_per_slice) - kb;  // >= 1 by the choice of slices
@@ -290,7 +315,7 @@ __global__ __launch_bounds__(256) void lowrank_tile_kernel(const uint16_t* __res
   static_for<P>([&](auto uu) { step(n_pad - P + decltype(uu)::value, uu, std::false_type{}); });
 
   // D rows = ranks j0 + 16 (wr TRW + a) + 4*(lane/16) + 0..3, column = token m0 + 16 (wm TMW + i) + lane%16
-  float* pz = part + (size_t)blockIdx.z * M * r;
+  float* pz = part + (size_t)blockIdx.z * slice_rows * r;
 #pragma unroll
   for (int a = 0; a < TRW; ++a) {
     const int j = j0 + 16 * (wr * TRW + a) + 4 * quad;
@@ -380,10 +405,11 @@ void launch_part(const LowrankShape& sh, const void* X, const void* V, int64_t M
   const dim3 grid = part_grid(sh, M, r);
   if (sh.steps_per_slice >= 16)
     lowrank_bf16_kernel<TF, RF, 4, 4><<<grid, dim3(256), 0, stream>>>((const uint16_t*)X, (const uint16_t*)V, (int)M,
-                                                                    (int)n_in, (int)r, sh.steps_per_slice, part);
+                                                                    (int)n_in, (int)r, sh.steps_per_slice, part, Groups{});
   else
     lowrank_bf16_kernel<TF, RF, 4, 2><<<grid, dim3(256), 0, stream>>>((const uint16_t*)X, (const uint16_t*)V, (int)M,
-                                                                    (int)n_in, (int)r, sh.steps_per_slice, part);
+                                                                    (int)n_in, (int)r, sh.steps_per_slice, part,
+                                                                    Groups{});
 }
 
 template <int TMW>
@@ -391,7 +417,8 @@ void launch_tile(const LowrankShape& sh, const void* X, const void* V, int64_t M
                  float* part, hipStream_t stream) {
   const dim3 grid = tile_grid(sh, M, r);
   lowrank_tile_kernel<TMW, 2, 1, 4, 4><<<grid, dim3(256), 0, stream>>>(
-      (const uint16_t*)X, (const uint16_t*)V, (int)M, (int)n_in, (int)r, cdiv(r, 128), sh.steps_per_slice, part);
+      (const uint16_t*)X, (const uint16_t*)V, (int)M, (int)n_in, (int)r, cdiv(r, 128), sh.steps_per_slice, part,
+      Groups{});
 }
 
 }  // namespace
@@ -432,6 +459,82 @@ hipError_t launch_lowrank(const void* X, const void* V, int64_t M, int64_t n_in,
   } else {
     lowrank_f32_kernel<<<f32_grid(M, r), dim3(256), 0, stream>>>(
         (const float*)X, (const float*)V, (int)M, (int)n_in, (int)r, part);
+  }
+  return hipGetLastError();
+}
+
+namespace {
+
+// The experts' first stage: the shapes above, by the rows an expert has on average, with K cut into
+// slices as far as the token blocks of all experts (each expert's last one counted) leave CUs idle.
+LowrankShape experts_shape(const FusedCall& c, int64_t& blocks) {
+  constexpr int64_t kWant = 256;
+  LowrankShape sh{};
+  const int64_t TK = (c.n_in + 63) / 64, mean = ceil_div(c.M, c.experts);
+  int64_t per_block, others;
+  if (mean <= 16 || c.r <= 64) {
+    sh.tf = mean <= 16 ? 1 : 2;
+    sh.rf = (mean > 16 && c.r % 32 == 0) ? 2 : 1;
+    per_block = 16 * sh.tf;
+    others = c.r / (16 * sh.rf);
+  } else {
+    sh.tile = true;
+    sh.bm = mean >= 512 ? 64 : 32;
+    per_block = sh.bm;
+    others = ceil_div(c.r, 128);
+  }
+  blocks = most_group_tiles(c.M, c.experts, per_block);
+  const int64_t most = std::min<int64_t>(mean <= 16 ? kDecodeMaxSlices : kMaxLowrankSlices, TK);
+  const int64_t slices = std::min(most, std::max<int64_t>(1, ceil_div(kWant, blocks * others)));
+  sh.steps_per_slice = (int)ceil_div(TK, slices);
+  sh.slices = (int)ceil_div(TK, sh.steps_per_slice);
+  return sh;
+}
+
+dim3 experts_grid(const LowrankShape& sh, int64_t blocks, int64_t r) {
+  if (sh.tile) return dim3((unsigned)(ceil_div(r, 128) * blocks), 1u, (unsigned)sh.slices);
+  return dim3((unsigned)blocks, (unsigned)(r / (16 * sh.rf)), (unsigned)sh.slices);
+}
+
+}  // namespace
+
+int experts_lowrank_slices(const FusedCall& c) {
+  int64_t blocks;
+  return experts_shape(c, blocks).slices;
+}
+
+bool experts_lowrank_grid_fits(const FusedCall& c) {
+  int64_t blocks;
+  const LowrankShape sh = experts_shape(c, blocks);
+  return grid_fits(experts_grid(sh, blocks, c.r), 256);
+}
+
+hipError_t launch_experts_lowrank(const FusedCall& c, hipStream_t stream) {
+  int64_t blocks;
+  const LowrankShape sh = experts_shape(c, blocks);
+  const dim3 grid = experts_grid(sh, blocks, c.r);
+  const Groups groups{c.offsets, (int)c.experts, (int)c.M};
+  const auto part = [&](auto kernel) {
+    kernel<<<grid, dim3(256), 0, stream>>>((const uint16_t*)c.X, (const uint16_t*)c.V, (int)c.M, (int)c.n_in, (int)c.r,
+                                           sh.steps_per_slice, (float*)c.workspace, groups);
+  };
+  const auto tile = [&](auto kernel) {
+    kernel<<<grid, dim3(256), 0, stream>>>((const uint16_t*)c.X, (const uint16_t*)c.V, (int)c.M, (int)c.n_in, (int)c.r,
+                                           cdiv(c.r, 128), sh.steps_per_slice, (float*)c.workspace, groups);
+  };
+  const bool deep = sh.steps_per_slice >= 16;
+  if (sh.tile) {
+    if (sh.bm == 64) tile(lowrank_tile_kernel<4, 2, 1, 4, 4, true>);
+    else tile(lowrank_tile_kernel<2, 2, 1, 4, 4, true>);
+  } else if (sh.tf == 1) {
+    if (deep) part(lowrank_bf16_kernel<1, 1, 4, 4, true>);
+    else part(lowrank_bf16_kernel<1, 1, 4, 2, true>);
+  } else if (sh.rf == 2) {
+    if (deep) part(lowrank_bf16_kernel<2, 2, 4, 4, true>);
+    else part(lowrank_bf16_kernel<2, 2, 4, 2, true>);
+  } else {
+    if (deep) part(lowrank_bf16_kernel<2, 1, 4, 4, true>);
+    else part(lowrank_bf16_kernel<2, 1, 4, 2, true>);
   }
   return hipGetLastError();
 }

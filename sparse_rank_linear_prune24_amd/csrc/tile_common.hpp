@@ -63,9 +63,10 @@ struct TPairBuilder {
   size_t stride;
   int slices, tid;
 
+  // t_rows: the rows of a slice where they are more than M (T of all experts' rows, Tpart at this one's)
   __device__ __forceinline__ void init(const float* __restrict__ Tpart, int n_slices, int M, int r, int m0, int j0,
-                                       int t) {
-    stride = (size_t)M * r;
+                                       int t, int t_rows = 0) {
+    stride = (size_t)(t_rows ? t_rows : M) * r;
     slices = n_slices;
     tid = t;
 #pragma unroll
@@ -119,9 +120,9 @@ struct TPairBuilder {
 
 template <int ROWS, int NT>
 __device__ __forceinline__ void build_t_pair(const float* __restrict__ Tpart, int slices, int M, int r, int m0,
-                                             int j0, u32x4_t* hi, u32x4_t* lo, int tid) {
+                                             int j0, u32x4_t* hi, u32x4_t* lo, int tid, int t_rows = 0) {
   TPairBuilder<ROWS, NT> tb;
-  tb.init(Tpart, slices, M, r, m0, j0, tid);
+  tb.init(Tpart, slices, M, r, m0, j0, tid, t_rows);
   tb.issue(0);
   __builtin_amdgcn_sched_barrier(0);
   tb.finish(hi, lo);

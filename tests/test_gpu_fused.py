@@ -100,6 +100,16 @@ def test_in_place(dtype, M, y_dtype):
         assert got is e[name] and torch.equal(got, want), name
 
 
+def test_without_epilogue_is_linear_ex():
+    """With nothing in the epilogue the bfloat16 product is linear_ex's, bit for bit."""
+    for M in (7, 50, 200):
+        d, _, _ = case(M, 544, 200, 32, "bf16", F32, "none", False, False, False, seed=M)
+        for y in (F32, BF16):
+            a = run(d, "none", y, 200)
+            b = binding.linear_ex(d["X"], d["values"], d["meta"], d["U"], d["V"], y_dtype=y, n_out=200)
+            assert torch.equal(a, b), (M, y)
+
+
 @pytest.mark.parametrize("dtype,M", [("bf16", 5), ("bf16", 130), ("fp32", 130)])
 def test_not_finite_rows_stay_apart(dtype, M):
     """A token row, a gate entry or a residual entry that is not finite changes no other row or entry;
