@@ -13,7 +13,6 @@ explicitly where it cannot be read off U.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 from typing import List, Optional, Sequence, Tuple
@@ -487,23 +486,103 @@ class _Epilogue(ctypes.Structure):
     _fields_ = [("activation", _I32), ("bias", _P), ("gate", _P), ("residual", _P)]
 
 
-def _epilogue(X, M, n_out, bias, bias_shape, activation, gate, residual, y_dtype):
-    """Checks the epilogue's operands and returns them as the C struct."""
-    if activation not in ACTIVATIONS:
+def _is(t: torch.Tensor, dtype: torch.dtype, shape, index: int) -> bool:
+    """Whether `t` is a contiguous `dtype` tensor of `shape` on device number `index` (what `_expect`
+    checks with a message each; a serving loop's calls are mostly right, so they are asked this first)."""
+    return t.get_device() == index and t.dtype is dtype and t.shape == shape and t.is_contiguous()
+
+
+def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
+    return None if t is None else t.data_ptr()
+
+
+def _fused_call(X, offsets, values, meta, U, V, bias, activation, gate, residual, y_dtype, n_out, out, workspace,
+                stream):
+    """linear_fused (offsets None) and linear_experts: checks every tensor, allocates what is missing
+    on the call's stream and calls the library. X's device is the current one."""
+    M, n_in = _matrix(X, "X")
+    code = _dtype_code(X)
+    dt, device, index = X.dtype, X.device, X.get_device()
+    if not X.is_contiguous():
+        raise ValueError("X must be contiguous")
+    if stream is not None and getattr(stream, "device", device) != device:
+        raise ValueError(f"the stream belongs to {stream.device}, X to {device}")
+    act = ACTIVATIONS.get(activation)
+    if act is None:
         raise ValueError(f"activation must be one of {', '.join(ACTIVATIONS)}, got {activation!r}")
-    if y_dtype not in (torch.float32, torch.bfloat16):
+    if y_dtype is torch.bfloat16:
+        ycode = SPLR_BF16
+    elif y_dtype is torch.float32:
+        ycode = SPLR_FP32
+    else:
         raise ValueError(f"y_dtype must be float32 or bfloat16, got {y_dtype}")
-    if bias is not None:
-        _expect(bias, "bias", X.dtype, bias.numel(), X.device, bias_shape)
-    for t, name in ((gate, "gate"), (residual, "residual")):
-        if t is not None:
-            _expect(t, name, y_dtype, M * n_out, X.device, (M, n_out))
-    return _Epilogue(ACTIVATIONS[activation], _dev(bias, "bias"), _dev(gate, "gate"), _dev(residual, "residual"))
+    experts, E, lead = offsets is not None, 1, ()
+    if experts:
+        if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1 or not 2 <= offsets.numel() <= EXPERTS_MAX + 1:
+            raise ValueError(f"offsets must be a vector of 2 .. {EXPERTS_MAX + 1} entries")
+        E = offsets.numel() - 1
+        lead = (E,)
+        if not _is(offsets, torch.int32, (E + 1,), index):
+            _expect(offsets, "offsets", torch.int32, E + 1, device)
+    if values is None or meta is None:
+        raise ValueError("values and meta are required")
+    if n_out is None:
+        n_out = U.shape[-2] if U is not None and U.dim() > 1 else values.shape[len(lead)] * 16
+    TR, TK = (n_out + 15) // 16, (n_in + 63) // 64
+    if not _is(values, dt, (*lead, TR, TK, 64, 8), index):
+        _expect(values, "values", dt, E * TR * TK * 512, device)
+    if not _is(meta, torch.int32, (*lead, TR, (TK + 7) // 8, 64, 4), index):
+        _expect(meta, "meta", torch.int32, E * _meta_words(n_out, n_in), device)
+    if (U is None) != (V is None):
+        raise ValueError("U and V are given together (or neither, for no low-rank part)")
+    r = 0
+    if U is not None:
+        r = U.shape[-1] if U.dim() == 2 + len(lead) else -1
+        if not _is(U, dt, (*lead, n_out, r), index):
+            _expect(U, "U", dt, E * n_out * max(r, 0), device, (*lead, n_out, r))
+        if not _is(V, dt, (*lead, r, n_in), index):
+            _expect(V, "V", dt, E * max(r, 0) * n_in, device, (*lead, r, n_in))
+    if bias is not None and not _is(bias, dt, (*lead, n_out), index):
+        _expect(bias, "bias", dt, E * n_out, device, (*lead, n_out))
+    rows = (M, n_out)
+    if gate is not None and not _is(gate, y_dtype, rows, index):
+        _expect(gate, "gate", y_dtype, M * n_out, device, rows)
+    if residual is not None and not _is(residual, y_dtype, rows, index):
+        _expect(residual, "residual", y_dtype, M * n_out, device, rows)
+    L = lib()
+    the_stream = torch.cuda.current_stream() if stream is None else stream
+    if out is None or (workspace is None and r > 0):
+        with torch.cuda.stream(the_stream):
+            if out is None:
+                out = torch.empty(rows, dtype=y_dtype, device=device)
+            if workspace is None and r > 0:
+                need = (L.splr_linear_experts_workspace_bytes(M, E, n_out, n_in, r, code) if experts else
+                        L.splr_linear_workspace_bytes(M, n_out, n_in, r, code))
+                workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    if not _is(out, y_dtype, rows, index):
+        _expect(out, "out", y_dtype, M * n_out, device, rows)
+    ws_bytes = 0
+    if workspace is not None:
+        if not _is_device(workspace) or workspace.get_device() != index or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous tensor on the device of X")
+        ws_bytes = workspace.nbytes
+    epilogue = _Epilogue(act, _ptr(bias), _ptr(gate), _ptr(residual))
+    layer = (values.data_ptr(), meta.data_ptr(), n_out, _ptr(U), _ptr(V), r, code, ctypes.byref(epilogue), ycode,
+             out.data_ptr(), _ptr(workspace), ws_bytes, the_stream.cuda_stream)
+    if experts:
+        _check("splr_linear_experts",
+               L.splr_linear_experts(X.data_ptr(), M, n_in, offsets.data_ptr(), E, *layer))
+    else:
+        _check("splr_linear_fused", L.splr_linear_fused(X.data_ptr(), M, n_in, *layer))
+    return out
 
 
-def _on_device_of(t: torch.Tensor):
-    """The device of `t` made current for the call: its streams and launches belong to it."""
-    return torch.cuda.device(t.device) if t.is_cuda else contextlib.nullcontext()
+def _fused_on_device(X, *args):
+    """_fused_call with X's device current (its streams and launches belong to it)."""
+    if isinstance(X, torch.Tensor) and X.is_cuda and X.get_device() != torch.cuda.current_device():
+        with torch.cuda.device(X.device):
+            return _fused_call(X, *args)
+    return _fused_call(X, *args)
 
 
 def linear_fused(X: torch.Tensor, values: torch.Tensor, meta: torch.Tensor, U: Optional[torch.Tensor],
@@ -516,17 +595,8 @@ def linear_fused(X: torch.Tensor, values: torch.Tensor, meta: torch.Tensor, U: O
     after the products in the kernels' epilogue (splr_linear_fused). bias [n_out] of X's type; gate
     and residual [M, n_out] of y_dtype; `out` may be gate or residual itself. The workspace is
     linear's (new_workspace)."""
-    M, n_in = _matrix(X, "X")
-    with _on_device_of(X):
-        M, n_in, n_out, r, out, workspace, ws_bytes = _linear_args(X, values, meta, U, V, n_out, out, workspace,
-                                                                   stream, y_dtype=y_dtype)
-        ep = _epilogue(X, M, n_out, bias, (n_out,), activation, gate, residual, y_dtype)
-        ycode = SPLR_BF16 if y_dtype == torch.bfloat16 else SPLR_FP32
-        _check("splr_linear_fused",
-               lib().splr_linear_fused(_dev(X, "X"), M, n_in, _dev(values, "values"), _dev(meta, "meta"), n_out,
-                                       _dev(U, "U"), _dev(V, "V"), r, _dtype_code(X), ctypes.byref(ep), ycode,
-                                       _dev(out, "out"), _dev(workspace, "workspace"), ws_bytes, _stream(stream)))
-    return out
+    return _fused_on_device(X, None, values, meta, U, V, bias, activation, gate, residual, y_dtype, n_out, out,
+                            workspace, stream)
 
 
 def experts_workspace_bytes(M: int, n_experts: int, n_out: int, n_in: int, r: int, dtype: torch.dtype) -> int:
@@ -547,45 +617,10 @@ def linear_experts(X: torch.Tensor, offsets: torch.Tensor, values: torch.Tensor,
     only, so nothing waits for it. values (E, TR, TK, 64, 8) and meta (E, TR, TKB, 64, 4): the experts'
     packed S one after the other; U [E, n_out, r], V [E, r, n_in], bias [E, n_out]. M may be 0. Rows
     outside offsets[0] .. offsets[E]-1 of `out` are left as they were."""
-    M, n_in = _matrix(X, "X")
-    _dtype_code(X)
-    if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1 or not 2 <= offsets.numel() <= EXPERTS_MAX + 1:
-        raise ValueError(f"offsets must be a vector of 2 .. {EXPERTS_MAX + 1} entries")
-    E = offsets.numel() - 1
-    _expect(offsets, "offsets", torch.int32, E + 1, X.device)
-    if n_out is None:
-        n_out = U.shape[1] if U is not None and U.dim() == 3 else values.shape[1] * 16
-    TR, TK = tiles(n_out, n_in)
-    _expect(values, "values", X.dtype, E * TR * TK * 512, X.device)
-    _expect(meta, "meta", torch.int32, E * _meta_words(n_out, n_in), X.device)
-    if (U is None) != (V is None):
-        raise ValueError("U and V are given together (or neither, for no low-rank part)")
-    r = 0
-    if U is not None:
-        r = U.shape[2] if U.dim() == 3 else -1
-        _expect(U, "U", X.dtype, E * n_out * max(r, 0), X.device, (E, n_out, r))
-        _expect(V, "V", X.dtype, E * max(r, 0) * n_in, X.device, (E, r, n_in))
-    ep = _epilogue(X, M, n_out, bias, (E, n_out), activation, gate, residual, y_dtype)
-    with _on_device_of(X):
-        need = experts_workspace_bytes(M, E, n_out, n_in, r, X.dtype)
-        if out is None or (workspace is None and need):
-            with torch.cuda.stream(_the_stream(stream)):
-                if out is None:
-                    out = torch.empty((M, n_out), dtype=y_dtype, device=X.device)
-                if workspace is None and need:
-                    workspace = torch.empty(need, dtype=torch.uint8, device=X.device)
-        _expect(out, "out", y_dtype, M * n_out, X.device, (M, n_out))
-        if workspace is not None and (not _is_device(workspace) or workspace.device != X.device
-                                      or not workspace.is_contiguous()):
-            raise ValueError("workspace must be a contiguous tensor on the device of X")
-        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-        ycode = SPLR_BF16 if y_dtype == torch.bfloat16 else SPLR_FP32
-        _check("splr_linear_experts",
-               lib().splr_linear_experts(_dev(X, "X"), M, n_in, _dev(offsets, "offsets"), E, _dev(values, "values"),
-                                         _dev(meta, "meta"), n_out, _dev(U, "U"), _dev(V, "V"), r, _dtype_code(X),
-                                         ctypes.byref(ep), ycode, _dev(out, "out"), _dev(workspace, "workspace"),
-                                         ws_bytes, _stream(stream)))
-    return out
+    if offsets is None:
+        raise ValueError("offsets is required")
+    return _fused_on_device(X, offsets, values, meta, U, V, bias, activation, gate, residual, y_dtype, n_out, out,
+                            workspace, stream)
 
 
 def dense_reconstruct(values: torch.Tensor, meta: torch.Tensor, U: Optional[torch.Tensor],
