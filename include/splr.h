@@ -334,7 +334,10 @@ splr_status_t splr_linear_noalloc(const void* X, int64_t M, int64_t n_in, const 
  * (LoSparse page, section 3.2, for the two products).  Everything after the products is evaluated in
  * float32 and rounded once, to y_dtype, when Y is stored, so no intermediate matrix goes to memory.
  *
- *   X, values, meta, U, V, r, workspace          as for splr_linear
+ *   X, values, meta, U, V, r                     as for splr_linear
+ *   workspace  splr_linear_fused_workspace_bytes() bytes (0 when r == 0; for bfloat16 what
+ *              splr_linear needs), clobbered; its contents on entry do not matter.  Two calls that
+ *              may run at the same time need one each.
  *   epilogue   NULL, or the operands below; a NULL operand is left out
  *     activation   act, applied to Z
  *     bias         [n_out] dtype, added to every row
@@ -342,7 +345,10 @@ splr_status_t splr_linear_noalloc(const void* X, int64_t M, int64_t n_in, const 
  *     residual     [M][n_out] y_dtype, added last
  *   Y          [M][n_out] y_dtype.  It may be the very buffer of gate or of residual (same address:
  *              every entry is read before it is written); it must not overlap anything else.
- * Arithmetic: float32 accumulation as splr_linear; bitwise reproducible run to run.
+ * Arithmetic: float32 accumulation as splr_linear; bitwise reproducible run to run.  With SPLR_FP32
+ *         the sparse product runs on the bfloat16 matrix cores with every operand as the exact sum of
+ *         three bfloat16 numbers; of the nine partial products the three below 2^-23 of the whole are
+ *         left out.  Its error is that of a float32 sum; an infinite X or S entry gives NaN.
  * Errors: as splr_linear_ex; epilogue operands misaligned -> SPLR_ERR_ALIGN; activation unknown ->
  *         SPLR_ERR_SHAPE.
  */
@@ -353,6 +359,8 @@ typedef struct {
   const void* residual;
 } splr_epilogue_t;
 
+size_t splr_linear_fused_workspace_bytes(int64_t M, int64_t n_out, int64_t n_in, int64_t r,
+                                         splr_dtype_t dtype);
 splr_status_t splr_linear_fused(const void* X, int64_t M, int64_t n_in, const void* values,
                                 const uint32_t* meta, int64_t n_out, const void* U, const void* V,
                                 int64_t r, splr_dtype_t dtype, const splr_epilogue_t* epilogue,

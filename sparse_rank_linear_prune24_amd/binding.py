@@ -28,7 +28,7 @@ STATUS = {0: "SPLR_OK", 1: "SPLR_ERR_NULL", 2: "SPLR_ERR_SHAPE", 3: "SPLR_ERR_DT
 EXPORTS = ("splr_prune24_pack", "splr_prune_nm_pack", "splr_linear_ex", "splr_prune24_pack_scaled", "splr_prune24_pack_residual", "splr_packed_bytes", "splr_linear_workspace_bytes", "splr_linear",
            "splr_linear_stage1", "splr_linear_stage2", "splr_linear_stage2_dense", "splr_linear_group",
            "splr_linear_stage2_group", "splr_linear_noalloc", "splr_linear_fused", "splr_linear_experts",
-           "splr_linear_experts_workspace_bytes", "splr_dense_reconstruct",
+           "splr_linear_fused_workspace_bytes", "splr_linear_experts_workspace_bytes", "splr_dense_reconstruct",
            "splr_gram_workspace_bytes", "splr_gram_f64", "splr_chol_rinv", "splr_status_string", "splr_version")
 
 _P, _I64, _I32, _SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t
@@ -78,6 +78,8 @@ def lib() -> ctypes.CDLL:
         L.splr_linear_noalloc.restype = _I32
         L.splr_linear_fused.argtypes = [_P, _I64, _I64, _P, _P, _I64, _P, _P, _I64, _I32, _P, _I32, _P, _P, _SZ, _P]
         L.splr_linear_fused.restype = _I32
+        L.splr_linear_fused_workspace_bytes.argtypes = [_I64, _I64, _I64, _I64, _I32]
+        L.splr_linear_fused_workspace_bytes.restype = _SZ
         L.splr_linear_experts_workspace_bytes.argtypes = [_I64, _I64, _I64, _I64, _I64, _I32]
         L.splr_linear_experts_workspace_bytes.restype = _SZ
         L.splr_linear_experts.argtypes = [_P, _I64, _I64, _P, _I64, _P, _P, _I64, _P, _P, _I64, _I32, _P, _I32, _P,
@@ -557,7 +559,7 @@ def _fused_call(X, offsets, values, meta, U, V, bias, activation, gate, residual
                 out = torch.empty(rows, dtype=y_dtype, device=device)
             if workspace is None and r > 0:
                 need = (L.splr_linear_experts_workspace_bytes(M, E, n_out, n_in, r, code) if experts else
-                        L.splr_linear_workspace_bytes(M, n_out, n_in, r, code))
+                        L.splr_linear_fused_workspace_bytes(M, n_out, n_in, r, code))
                 workspace = torch.empty(need, dtype=torch.uint8, device=device)
     if not _is(out, y_dtype, rows, index):
         _expect(out, "out", y_dtype, M * n_out, device, rows)
@@ -593,10 +595,15 @@ def linear_fused(X: torch.Tensor, values: torch.Tensor, meta: torch.Tensor, U: O
                  stream=None) -> torch.Tensor:
     """Y [M, n_out] of y_dtype = act(X S^T + (X V^T) U^T + bias) * gate + residual, with everything
     after the products in the kernels' epilogue (splr_linear_fused). bias [n_out] of X's type; gate
-    and residual [M, n_out] of y_dtype; `out` may be gate or residual itself. The workspace is
-    linear's (new_workspace)."""
+    and residual [M, n_out] of y_dtype; `out` may be gate or residual itself. The workspace holds
+    fused_workspace_bytes()."""
     return _fused_on_device(X, None, values, meta, U, V, bias, activation, gate, residual, y_dtype, n_out, out,
                             workspace, stream)
+
+
+def fused_workspace_bytes(M: int, n_out: int, n_in: int, r: int, dtype: torch.dtype) -> int:
+    code = SPLR_BF16 if dtype == torch.bfloat16 else SPLR_FP32
+    return int(lib().splr_linear_fused_workspace_bytes(M, n_out, n_in, r, code))
 
 
 def experts_workspace_bytes(M: int, n_experts: int, n_out: int, n_in: int, r: int, dtype: torch.dtype) -> int:

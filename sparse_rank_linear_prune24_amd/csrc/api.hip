@@ -311,17 +311,31 @@ splr::FusedCall fused_call(const void* X, int64_t M, int64_t n_in, const int32_t
                          y_dtype == SPLR_BF16, workspace, 1};
 }
 
-size_t experts_workspace_bytes(const splr::FusedCall& c) { return round_up(splr::fused_workspace_bytes(c), 256); }
+size_t call_workspace_bytes(const splr::FusedCall& c) { return round_up(splr::fused_workspace_bytes(c), 256); }
+
+splr_status_t check_fused_workspace(const splr::FusedCall& c, size_t ws_bytes) {
+  const size_t need = call_workspace_bytes(c);
+  if (need > 0 && (!c.workspace || ws_bytes < need)) return SPLR_ERR_WORKSPACE;
+  if (need > 0 && !aligned16(c.workspace)) return SPLR_ERR_ALIGN;
+  return SPLR_OK;
+}
 
 }  // namespace
 
 extern "C" {
 
+size_t splr_linear_fused_workspace_bytes(int64_t M, int64_t n_out, int64_t n_in, int64_t r, splr_dtype_t dtype) {
+  if (M < 1 || M > kMaxRows || check_in(n_in) != SPLR_OK || check_rank(r) != SPLR_OK || !dtype_ok(dtype)) return 0;
+  return call_workspace_bytes(fused_call(nullptr, M, n_in, nullptr, 1, nullptr, nullptr, n_out, nullptr, nullptr, r,
+                                          dtype, splr::Epilogue{}, nullptr, SPLR_FP32, nullptr));
+}
+
 splr_status_t splr_linear_fused(const void* X, int64_t M, int64_t n_in, const void* values, const uint32_t* meta,
                                 int64_t n_out, const void* U, const void* V, int64_t r, splr_dtype_t dtype,
                                 const splr_epilogue_t* epilogue, splr_dtype_t y_dtype, void* Y, void* workspace,
                                 size_t ws_bytes, hipStream_t stream) {
-  splr_status_t s = check_linear(X, M, n_in, values, meta, n_out, U, V, r, dtype, Y, workspace, ws_bytes, true, true);
+  splr_status_t s =
+      check_linear(X, M, n_in, values, meta, n_out, U, V, r, dtype, Y, nullptr, 0, true, true, false);
   if (s != SPLR_OK) return s;
   splr::Epilogue ep;
   s = check_epilogue(epilogue, dtype, y_dtype, &ep);
@@ -329,6 +343,8 @@ splr_status_t splr_linear_fused(const void* X, int64_t M, int64_t n_in, const vo
   const splr::FusedCall c =
       fused_call(X, M, n_in, nullptr, 1, values, meta, n_out, U, V, r, dtype, ep, Y, y_dtype, workspace);
   if (!splr::fused_grids_fit(c)) return SPLR_ERR_SHAPE;
+  s = check_fused_workspace(c, ws_bytes);
+  if (s != SPLR_OK) return s;
   return from_hip(splr::launch_fused(c, stream));
 }
 
@@ -338,7 +354,7 @@ size_t splr_linear_experts_workspace_bytes(int64_t M, int64_t n_experts, int64_t
       check_rank(r) != SPLR_OK || !dtype_ok(dtype))
     return 0;
   const int32_t any = 0;  // a non-null `offsets`: a call by expert
-  return experts_workspace_bytes(fused_call(nullptr, M, n_in, &any, n_experts, nullptr, nullptr, n_out, nullptr,
+  return call_workspace_bytes(fused_call(nullptr, M, n_in, &any, n_experts, nullptr, nullptr, n_out, nullptr,
                                             nullptr, r, dtype, splr::Epilogue{}, nullptr, SPLR_FP32, nullptr));
 }
 
@@ -368,9 +384,8 @@ splr_status_t splr_linear_experts(const void* X, int64_t M, int64_t n_in, const 
   const splr::FusedCall c =
       fused_call(X, M, n_in, offsets, n_experts, values, meta, n_out, U, V, r, dtype, ep, Y, y_dtype, workspace);
   if (!splr::fused_grids_fit(c)) return SPLR_ERR_SHAPE;
-  const size_t need = experts_workspace_bytes(c);
-  if (need > 0 && (!workspace || ws_bytes < need)) return SPLR_ERR_WORKSPACE;
-  if (need > 0 && !aligned16(workspace)) return SPLR_ERR_ALIGN;
+  s = check_fused_workspace(c, ws_bytes);
+  if (s != SPLR_OK) return s;
   return from_hip(splr::launch_fused(c, stream));
 }
 

@@ -105,6 +105,10 @@ int experts_lowrank_slices(const FusedCall& c);
 hipError_t launch_experts_lowrank(const FusedCall& c, hipStream_t stream);
 hipError_t launch_fused_prefill(const FusedCall& c, hipStream_t stream);
 hipError_t launch_fused_decode(const FusedCall& c, int tokens, hipStream_t stream);
+// Both stages in float32 (tokens as for the decode kernel, 0: the tile kernel).
+int fused_f32_slices(const FusedCall& c);
+bool fused_f32_grids_fit(const FusedCall& c, int tokens);
+hipError_t launch_fused_f32(const FusedCall& c, int tokens, hipStream_t stream);
 bool fused_prefill_grid_fits(const FusedCall& c);
 bool experts_lowrank_grid_fits(const FusedCall& c);
 

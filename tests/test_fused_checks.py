@@ -63,8 +63,16 @@ def test_workspace_sizes():
         assert f(*bad) == 0
     need = f(64, 4, 32, 64, 16, 1)
     assert experts(M=64, wsb=need - 1) == WORKSPACE
-    need = binding.lib().splr_linear_workspace_bytes(64, 32, 64, 16, 1)
-    assert fused(M=64, wsb=need - 1) == WORKSPACE
+    f = binding.lib().splr_linear_fused_workspace_bytes
+    assert f(64, 32, 64, 0, 1) == 0
+    for bad in ((0, 32, 64, 16, 1), (64, 32, 48, 16, 1), (64, 32, 64, 8, 1), (64, 32, 64, 16, 3)):
+        assert f(*bad) == 0
+    for dt in (0, 1):
+        for M, K, r in ((64, 64, 16), (1, 4096, 64), (500, 14336, 128), (8192, 4096, 64)):
+            need = f(M, 32, K, r, dt)
+            assert need >= M * r * 4 and fused(M=M, K=K, r=r, dt=dt, wsb=need - 1) == WORKSPACE
+            if dt == 1:
+                assert need == binding.lib().splr_linear_workspace_bytes(M, 32, K, r, dt)
 
 
 # ----------------------------------------------------------------------------- the binding

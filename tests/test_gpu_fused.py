@@ -139,7 +139,7 @@ def test_graph_replays_and_streams(dtype, M):
     cases = [case(M, 1056, 200, 64, dtype, BF16, "silu", True, True, True, seed=s)[0] for s in (1, 2, 3)]
     want = [run(c, "silu", BF16, 200) for c in cases]
     live = {k: v.clone() for k, v in cases[0].items()}
-    ws = binding.new_workspace(M, 200, 1056, 64, live["X"].dtype)
+    ws = torch.empty(binding.fused_workspace_bytes(M, 200, 1056, 64, live["X"].dtype), dtype=torch.uint8, device="cuda")
     out = torch.empty_like(want[0])
     s = torch.cuda.Stream()
     torch.cuda.synchronize()
