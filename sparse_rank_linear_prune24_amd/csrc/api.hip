@@ -288,7 +288,8 @@ namespace {
 
 // Checks the epilogue and turns it into the kernels' form.
 splr_status_t check_epilogue(const splr_epilogue_t* epilogue, splr_dtype_t dtype, splr_dtype_t y_dtype,
-                             splr::Epilogue* out) {
+                             int64_t n_out, splr::Epilogue* out) {
+  if (n_out > splr::kMaxFusedOut) return SPLR_ERR_SHAPE;
   if (!dtype_ok(y_dtype)) return SPLR_ERR_DTYPE;
   *out = splr::Epilogue{nullptr, nullptr, nullptr, splr::kActNone, dtype == SPLR_BF16 ? 1 : 0};
   if (!epilogue) return SPLR_OK;
@@ -338,7 +339,7 @@ splr_status_t splr_linear_fused(const void* X, int64_t M, int64_t n_in, const vo
       check_linear(X, M, n_in, values, meta, n_out, U, V, r, dtype, Y, nullptr, 0, true, true, false);
   if (s != SPLR_OK) return s;
   splr::Epilogue ep;
-  s = check_epilogue(epilogue, dtype, y_dtype, &ep);
+  s = check_epilogue(epilogue, dtype, y_dtype, n_out, &ep);
   if (s != SPLR_OK) return s;
   const splr::FusedCall c =
       fused_call(X, M, n_in, nullptr, 1, values, meta, n_out, U, V, r, dtype, ep, Y, y_dtype, workspace);
@@ -375,7 +376,7 @@ splr_status_t splr_linear_experts(const void* X, int64_t M, int64_t n_in, const 
   if (s != SPLR_OK) return s;
   if (!dtype_ok(dtype)) return SPLR_ERR_DTYPE;
   splr::Epilogue ep;
-  s = check_epilogue(epilogue, dtype, y_dtype, &ep);
+  s = check_epilogue(epilogue, dtype, y_dtype, n_out, &ep);
   if (s != SPLR_OK) return s;
   if (!aligned16(X) || !aligned16(values) || !aligned16(meta) || !aligned16(Y) ||
       (reinterpret_cast<uintptr_t>(offsets) & 3u) || (r > 0 && (!aligned16(U) || !aligned16(V))))

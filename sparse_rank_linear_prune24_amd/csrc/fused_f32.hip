@@ -21,8 +21,6 @@
 namespace splr {
 namespace {
 
-typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
-
 __device__ __forceinline__ f32x4_t mfma_f32(float a, float b, f32x4_t c) {
   return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0);
 }
@@ -38,7 +36,7 @@ __device__ __forceinline__ Parts8 split3(f32x4_t lo, f32x4_t hi) {
     f32x2_t x = i < 2 ? f32x2_t{lo[2 * i], lo[2 * i + 1]} : f32x2_t{hi[2 * i - 4], hi[2 * i - 3]};
 #pragma unroll
     for (int k = 0; k < 3; ++k) {
-      const uint32_t w = __builtin_bit_cast(uint32_t, __builtin_convertvector(x, bf16x2_t));
+      const uint32_t w = round_bf16x2(x[0], x[1]);
       o.p[k][i] = w;
       x[0] -= __uint_as_float(w << 16);
       x[1] -= __uint_as_float(w & 0xFFFF0000u);

@@ -75,6 +75,8 @@ hipError_t launch_linear_f32(const float* X, int64_t M, int64_t n_in, const floa
                              int64_t n_out, const float* U, int64_t r, const float* T, void* Y, bool y_bf16,
                              hipStream_t stream);
 
+// Most outputs of a fused call: a tile's 128 token rows of float32 Y span less than 2^31 bytes.
+constexpr int64_t kMaxFusedOut = int64_t(1) << 21;
 // The layer product with a fused epilogue: splr_linear_fused (offsets NULL, one expert) and
 // splr_linear_experts. A call's operands, as its launchers take them.
 struct FusedCall {

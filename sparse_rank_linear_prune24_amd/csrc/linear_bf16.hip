@@ -100,26 +100,92 @@ __device__ __forceinline__ void store_tile_rows_lds(const f32x4_t (&acc)[NI][NJ]
   }
 }
 
+// Word 3 of a raw buffer descriptor on gfx9-family GPUs: 32-bit data format, no swizzle, no index
+// stride (plain byte-addressed loads).
+constexpr int kBufferFlags = 0x00020000;
+
 // store_tile_rows_lds with the fused epilogue between the LDS buffer and Y: each lane finishes four
-// consecutive entries of a token row, with gate and residual read (and Y written) as whole rows. The
-// rounds over 32-token slices run as a loop, not unrolled, so that the activations' code exists once
-// (straight-line it would exceed the instruction cache); only the reads of the accumulators, which need
-// constant indexes, are per round. `row0` is the first token of the tile in Y, gate and residual.
+// consecutive entries of a token row, with gate and residual read (and Y written) as whole rows. A
+// round is 32 tokens; the gate and residual entries of the next round are requested as soon as the
+// present ones are used, so their latency is paid once, not per round. The rounds run as a loop, not
+// unrolled, so that the activations' code exists once; only the reads of the accumulators, which need
+// constant indexes, are per round. Gate, residual and Y are addressed alike: a descriptor over the
+// tile's token rows (which drops what lies behind the last one), one lane offset, one uniform offset per
+// read. `row0` is the first token of the tile in Y, gate and residual.
 template <int NI, int NJ, bool NT>
 __device__ __forceinline__ void store_tile_rows_fused(const f32x4_t (&acc)[NI][NJ], float* buf, const Epilogue& ep,
-                                                      size_t bias_row, void* Y, int y_bf16, int M, int n_out,
+                                                      size_t bias_row, void* Y, bool y_bf16, int M, int n_out,
                                                       int nrow0, int m0, size_t row0, int lane) {
   constexpr int R = 16 * NI, kPitch = R + 4, kTok = 32;
-  constexpr int kLanesPerTok = R / 4, kTokPerRead = 64 / kLanesPerTok, kBatch = 4;
-  static_assert(NJ % 2 == 0 && kTok % (kBatch * kTokPerRead) == 0, "32 tokens a round");
+  constexpr int kLanesPerTok = R / 4, kTokPerRead = 64 / kLanesPerTok, kReads = kTok / kTokPerRead;
+  constexpr int kAux = NT ? 2 : 0;  // nt
+  static_assert(NJ % 2 == 0, "32 tokens a round");
   const int q = lane >> 4, sb = lane & 15;
   const int rl = lane % kLanesPerTok, tl = lane / kLanesPerTok;
-  const int n = nrow0 + 4 * rl, left = n_out - n;
-  const bool vec = (n_out & 3) == 0 && left >= 4;
+  const int n = nrow0 + 4 * rl, left = n_out - n, rows = min(M - m0, 16 * NJ);
+  const int size = y_bf16 ? 2 : 4, pitch = n_out * size;  // n_out <= kMaxFusedOut: a tile stays below 2^31 bytes
+  const size_t first = row0 * pitch;
+  const auto descriptor = [&](const void* p) {
+    return __builtin_amdgcn_make_buffer_rsrc((void*)((const char*)p + first), (short)0, rows * pitch, kBufferFlags);
+  };
+  // every entry's own offset, past the descriptor's end where the row has no such entry
+  const bool vec = (n_out & 3) == 0;
+  const int off = left > 0 ? tl * pitch + n * size : 0x7FFFFFFF;
+  int off1[3];
+#pragma unroll
+  for (int e = 1; e < 4; ++e) off1[e - 1] = left > e ? off + e * size : 0x7FFFFFFF;
+  const auto load = [&](__amdgpu_buffer_rsrc_t p, int so) {
+    u32x4_t v = {0, 0, 0, 0};
+    if (vec) {
+      if (y_bf16) {
+        const u32x2_t w = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_raw_buffer_load_b64(p, off, so, 0));
+        v[0] = w[0];
+        v[1] = w[1];
+      } else {
+        v = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(p, off, so, 0));
+      }
+    } else if (y_bf16) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        v[e / 2] |= (uint32_t)(uint16_t)__builtin_amdgcn_raw_buffer_load_b16(p, e ? off1[e - 1] : off, so, 0) << (16 * (e & 1));
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = __builtin_amdgcn_raw_buffer_load_b32(p, e ? off1[e - 1] : off, so, 0);
+    }
+    return v;
+  };
+  const __amdgpu_buffer_rsrc_t y_rs = descriptor(Y), gate_rs = descriptor(ep.gate), res_rs = descriptor(ep.residual);
+  const auto store = [&](int so, f32x4_t y) {
+    if (y_bf16) {
+      const u32x2_t w = {round_bf16x2(y[0], y[1]), round_bf16x2(y[2], y[3])};
+      if (vec) {
+        __builtin_amdgcn_raw_buffer_store_b64(w, y_rs, off, so, kAux);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          __builtin_amdgcn_raw_buffer_store_b16((uint16_t)(w[e / 2] >> (16 * (e & 1))), y_rs, e ? off1[e - 1] : off, so, 0);
+      }
+    } else if (vec) {
+      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, y), y_rs, off, so, kAux);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(y[e]), y_rs, e ? off1[e - 1] : off, so, 0);
+    }
+  };
   f32x4_t bias = {0, 0, 0, 0};
   if (ep.bias && left > 0) bias = load4(ep.bias, bias_row + n, ep.bias_bf16, vec, left);
+  u32x4_t gate[kReads], residual[kReads];
+  // (a uniform offset never exceeds the descriptor's size: the range check subtracts it)
+  const auto request = [&](int token, int k) {
+    const int so = min(token, rows) * pitch;
+    if (ep.gate) gate[k] = load(gate_rs, so);
+    if (ep.residual) residual[k] = load(res_rs, so);
+  };
+#pragma unroll
+  for (int k = 0; k < kReads; ++k) request(k * kTokPerRead, k);
 #pragma unroll 1
-  for (int c = 0; c < NJ / 2; ++c) {
+  for (int c = 0; c < NJ / 2 && 32 * c < rows; ++c) {
     static_for<NJ / 2>([&](auto cc) {
       if (c == decltype(cc)::value) {
 #pragma unroll
@@ -129,30 +195,16 @@ __device__ __forceinline__ void store_tile_rows_fused(const f32x4_t (&acc)[NI][N
             *(f32x4_t*)(buf + (16 * jj + sb) * kPitch + 16 * i + 4 * q) = acc[i][2 * decltype(cc)::value + jj];
       }
     });
-    if (m0 + 32 * c >= M) break;
-#pragma unroll 1
-    for (int k = 0; k < kTok / kTokPerRead; k += kBatch) {
-      f32x4_t gate[kBatch], residual[kBatch];
 #pragma unroll
-      for (int b = 0; b < kBatch; ++b) {  // tokens past the last one read it again
-        const int t = min(32 * c + (k + b) * kTokPerRead + tl, M - 1 - m0);
-        const size_t at = (row0 + t) * n_out + n;
-        if (ep.gate && left > 0) gate[b] = load4(ep.gate, at, y_bf16, vec, left);
-        if (ep.residual && left > 0) residual[b] = load4(ep.residual, at, y_bf16, vec, left);
-      }
-#pragma unroll
-      for (int b = 0; b < kBatch; ++b) {
-        const int t = (k + b) * kTokPerRead + tl;
-        const f32x4_t y = finish4(*(const f32x4_t*)(buf + t * kPitch + 4 * rl), bias, ep, gate[b], residual[b]);
-        if (m0 + 32 * c + t < M && left > 0) store4<NT>(Y, (row0 + 32 * c + t) * n_out + n, y_bf16, vec, left, y);
-      }
+    for (int k = 0; k < kReads; ++k) {
+      const int token = 32 * c + k * kTokPerRead;
+      const f32x4_t sum = *(const f32x4_t*)(buf + (k * kTokPerRead + tl) * kPitch + 4 * rl);
+      const f32x4_t y = finish4(sum, bias, ep, widen4(gate[k], y_bf16), widen4(residual[k], y_bf16));
+      request(token + 32, k);  // behind the tile's last token: reads zeros
+      store(min(token, rows) * pitch, y);
     }
   }
 }
-
-// Word 3 of a raw buffer descriptor on gfx9-family GPUs: 32-bit data format, no swizzle, no index
-// stride (plain byte-addressed loads).
-constexpr int kBufferFlags = 0x00020000;
 
 // The structured-sparse MFMA with its accumulator pinned to the matrix-core accumulator registers
 // (the compiler would otherwise spread the accumulators over both register files and copy them
@@ -302,6 +354,13 @@ struct LayerGroup {
   const float* Tpart[kMaxGroup];
   void* Y[kMaxGroup];
 };
+// The same for a fused call, with what its epilogue needs
+struct FusedGroup : LayerGroup {
+  Epilogue ep;
+  Groups groups;
+  void* out;
+  int y_bf16;
+};
 template <typename T>
 __device__ __forceinline__ T pick_layer(const T (&a)[kMaxGroup], int layer) {
   static_assert(kMaxGroup == 4, "one compare per layer");
@@ -323,12 +382,29 @@ __device__ __forceinline__ T pick_layer(const T (&a)[kMaxGroup], int layer) {
 // then those of every expert's own rows, expert after expert, and the operands are shifted to the
 // expert of the tile (lg holds the first expert's, `layers` is 1).
 constexpr int kModePlain = 0, kModeFused = 1, kModeExperts = 2;
+template <int MODE>
+using ModeGroup = std::conditional_t<MODE == kModePlain, LayerGroup, FusedGroup>;
+
+// What the epilogue needs, read from the kernel's first argument only here, after the loop. Taken from the
+// argument as usual the compiler reads it at the kernel's start and keeps it in scalar registers
+// across the main loop, which then spills its own (8192 x 4096 -> 14336, gated: 857 against 0 us).
+struct LateArgs {
+  Epilogue ep;
+  void* out;
+  int y_bf16;
+};
+__device__ __forceinline__ LateArgs late_args() {
+  typedef const __attribute__((address_space(4))) char* Kernarg;
+  Kernarg p = (Kernarg)__builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(p));
+  const auto* g = (const __attribute__((address_space(4))) FusedGroup*)p;
+  return LateArgs{Epilogue{g->ep.bias, g->ep.gate, g->ep.residual, g->ep.act, g->ep.bias_bf16}, g->out, g->y_bf16};
+}
 
 template <int NI, int LA, int P, int EPI, int WAVES = 8, bool DENSE = false, int MODE = kModePlain>
 __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(WAVES / 4, WAVES / 4))) void
-linear_prefill_wide_kernel(const LayerGroup lg, int layers, int slices, int y_bf16, int M, int K, int n_out, int r,
-                           int tiles_n, int tiles_m, int tiles_per_xcd, int group_m, const Epilogue ep,
-                           const Groups groups) {
+linear_prefill_wide_kernel(const ModeGroup<MODE> lg, int layers, int slices, int y_bf16, int M, int K, int n_out, int r,
+                           int tiles_n, int tiles_m, int tiles_per_xcd, int group_m) {
   constexpr int NJ = 8, PX = 2;
   static_assert(WAVES == 4 || WAVES == 8, "one or two waves per SIMD");
   constexpr int BN = 16 * NI * WAVES;  // 512 or 256 rows
@@ -352,11 +428,11 @@ linear_prefill_wide_kernel(const LayerGroup lg, int layers, int slices, int y_bf
   // XCD-aware tile order: each XCD (own L2) runs a contiguous range of the tiles, layer after layer
   const int b = blockIdx.x;
   GroupTile gt = {0, 0, M, 0, tiles_m};
-  if constexpr (MODE == kModeExperts) tiles_per_xcd = (group_tiles_total<BM>(groups) * tiles_n + 7) / 8;
+  if constexpr (MODE == kModeExperts) tiles_per_xcd = (group_tiles_total<BM>(lg.groups) * tiles_n + 7) / 8;
   if (MODE == kModeExperts && (b >> 3) >= tiles_per_xcd) return;
   const int logical_all = (b & 7) * tiles_per_xcd + (b >> 3);
   if constexpr (MODE == kModeExperts) {
-    gt = find_group_tile<BM>(groups, logical_all / tiles_n);
+    gt = find_group_tile<BM>(lg.groups, logical_all / tiles_n);
     if (gt.expert < 0) return;
     tiles_m = gt.tiles;
     M = gt.rows;
@@ -372,7 +448,8 @@ linear_prefill_wide_kernel(const LayerGroup lg, int layers, int slices, int y_bf
   const uint16_t* __restrict__ U = pick_layer(lg.U, layer) + e * n_out * r;
   const float* __restrict__ Tpart = pick_layer(lg.Tpart, layer) + first_row * r;
   void* Y = pick_layer(lg.Y, layer);
-  const int t_rows = MODE == kModeExperts ? groups.rows : 0;
+  int t_rows = 0;
+  if constexpr (MODE == kModeExperts) t_rows = lg.groups.rows;
   const int per_group = group_m * tiles_n;
   const int g = logical / per_group;
   const int first_m = g * group_m;
@@ -424,15 +501,12 @@ linear_prefill_wide_kernel(const LayerGroup lg, int layers, int slices, int y_bf
   const int x_end = x_rows * K * 2, v_end = rows_here * s_stride, m_end = rows_here * m_stride;
   auto load_x = [&](int kc, u32x4_t (&v)[kXLoads]) {
     // half tail step: re-read valid columns (S is zero there); per lane, as the chunk decides
-    // (with the fused epilogue: read zeros, so that an infinite X entry is not multiplied by S's zero)
-    const bool tail = kc < TK && kc * 64 + 8 * xchunk >= K;
-    const int back = tail ? 64 : 0;
+    // (with the fused epilogue the lane's offset leaves the descriptor and reads zeros, so that an infinite
+    // X entry is not multiplied by S's zero)
+    const int back = (kc < TK && kc * 64 + 8 * xchunk >= K) ? (MODE == kModePlain ? 64 : -(1 << 30)) : 0;
     const int so = kc < TK ? kc * 128 : x_end;
 #pragma unroll
-    for (int t = 0; t < kXLoads; ++t) {
-      const int xo = MODE == kModePlain ? x_off[t] - back : tail ? x_end : x_off[t];
-      v[t] = __builtin_amdgcn_raw_buffer_load_b128(xrs, xo, so, 0);
-    }
+    for (int t = 0; t < kXLoads; ++t) v[t] = __builtin_amdgcn_raw_buffer_load_b128(xrs, x_off[t] - back, so, 0);
   };
   auto load_s_frag = [&](int kc, int i, u32x4_t& va) {
     va = __builtin_amdgcn_raw_buffer_load_b128(vrs, s_off, kc < TK ? i * s_stride + kc * 1024 : v_end, 0);
@@ -606,10 +680,13 @@ linear_prefill_wide_kernel(const LayerGroup lg, int layers, int slices, int y_bf
   accumulator_fence(acc);  // the last smfmac_acc results, before the stores
   if constexpr (MODE != kModePlain) {
     static_assert((EPI & kEpiRows) != 0 && WAVES * 32 * (16 * NI + 4) * 4 <= (int)sizeof(xs), "a private buffer per wave");
+    const LateArgs late = late_args();
+    int expert = gt.expert, row = gt.lo + m0;
+    asm volatile("" : "+s"(expert), "+s"(row));
     lds_barrier();
-    store_tile_rows_fused<NI, NJ, (EPI & kEpiDirectNT) != 0>(acc, (float*)xs + wave * 32 * (16 * NI + 4), ep,
-                                                            e * n_out, Y, y_bf16, M, n_out, nrow0, m0,
-                                                            first_row + m0, lane);
+    store_tile_rows_fused<NI, NJ, (EPI & kEpiDirectNT) != 0>(acc, (float*)xs + wave * 32 * (16 * NI + 4), late.ep,
+                                                            (size_t)expert * n_out, late.out, late.y_bf16, M, n_out,
+                                                            nrow0, m0, row, lane);
   } else if constexpr ((EPI & kEpiRows) != 0) {
     static_assert(WAVES * 32 * (16 * NI + 4) * 4 <= (int)sizeof(xs), "a private buffer per wave");
     lds_barrier();  // every wave's reads of the ring are done before it is reused
@@ -689,7 +766,7 @@ hipError_t launch_linear_bf16_group(int layers, const void* const* X, int64_t M,
   // 512-row tiles, 8 % on the 256-row tiles)
   const auto launch = [&](auto kernel) {
     kernel<<<grid, dim3(512), 0, stream>>>(lg, layers, slices, yb, (int)M, (int)n_in, (int)n_out, (int)r, tiles_n,
-                                           tiles_m, per_xcd, group_m, Epilogue{}, Groups{});
+                                           tiles_m, per_xcd, group_m);
   };
   if (BN == 512) {
     if (y_nt)
@@ -723,7 +800,7 @@ hipError_t launch_linear_bf16_dense(const void* X, int64_t M, int64_t n_in, cons
   const LayerGroup lg = make_group(1, &X, &values, &meta, &U, &Tpart, &Y);
   const auto args = [&](auto kernel, int waves) {
     kernel<<<grid, dim3(64 * waves), 0, stream>>>(lg, 1, slices, 0, (int)M, (int)n_in, (int)n_out, (int)r, tiles_n,
-                                                  tiles_m, per_xcd, group_m, Epilogue{}, Groups{});
+                                                  tiles_m, per_xcd, group_m);
   };
   if (BN == 512) {
     if (y_nt)
@@ -762,12 +839,12 @@ bool fused_prefill_grid_fits(const FusedCall& c) {
 hipError_t launch_fused_prefill(const FusedCall& c, hipStream_t stream) {
   const FusedTiles t = fused_tiles(c);
   const float* T = (const float*)c.workspace;
-  const LayerGroup lg = make_group(1, &c.X, &c.values, &c.meta, &c.U, &T, &c.Y);
+  const FusedGroup lg{make_group(1, &c.X, &c.values, &c.meta, &c.U, &T, &c.Y), c.ep,
+                      Groups{c.offsets, (int)c.experts, (int)c.M}, c.Y, c.y_bf16 ? 1 : 0};
   const bool y_nt = (double)c.M * c.n_out * (c.y_bf16 ? 2 : 4) > kNonTemporalYBytes;
   const auto launch = [&](auto kernel) {
     kernel<<<t.grid, dim3(512), 0, stream>>>(lg, 1, c.slices, c.y_bf16 ? 1 : 0, (int)c.M, (int)c.n_in, (int)c.n_out,
-                                             (int)c.r, t.tiles_n, t.tiles_m, (int)t.grid.x / 8, 4, c.ep,
-                                             Groups{c.offsets, (int)c.experts, (int)c.M});
+                                             (int)c.r, t.tiles_n, t.tiles_m, (int)t.grid.x / 8, 4);
   };
   const auto rows = [&](auto mode) {
     constexpr int kMode = decltype(mode)::value;
