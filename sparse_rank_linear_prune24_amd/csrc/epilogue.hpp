@@ -3,6 +3,8 @@
 // kernels of every size class.
 #pragma once
 
+#include <type_traits>
+
 #include "common.hpp"
 
 namespace splr {
@@ -45,23 +47,34 @@ __device__ __forceinline__ float gelu_logit(float z) {
   return z * fmaf(p, t, 1.5957697629928589f);
 }
 
-// act on four values; the switch is uniform, so it stays outside the values' code. gelu_tanh is
-// z sigma(2u), the same function as z (1 + tanh u) / 2 without its cancellation.
-__device__ __forceinline__ f32x4_t activate4(f32x4_t z, int act) {
-  if (act == kActNone) return z;
+// gelu_tanh is z sigma(2u), the same function as z (1 + tanh u) / 2 without its cancellation.
+template <int ACT>
+__device__ __forceinline__ f32x4_t activate4(f32x4_t z) {
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     const float v = z[e];
-    if (act == kActRelu)
-      z[e] = v < 0.0f ? 0.0f : v;
-    else if (act == kActGelu)
-      z[e] = v * logistic(gelu_logit(v));
-    else if (act == kActGeluTanh)
-      z[e] = v * logistic(1.5957691216057308f * fmaf(0.044715f * v * v, v, v));
-    else
-      z[e] = v * logistic(v);
+    if constexpr (ACT == kActRelu) z[e] = v < 0.0f ? 0.0f : v;
+    if constexpr (ACT == kActGelu) z[e] = v * logistic(gelu_logit(v));
+    if constexpr (ACT == kActGeluTanh) z[e] = v * logistic(1.5957691216057308f * fmaf(0.044715f * v * v, v, v));
+    if constexpr (ACT == kActSilu) z[e] = v * logistic(v);
   }
   return z;
+}
+// f(std::integral_constant<int, act>{})
+template <typename F>
+__device__ __forceinline__ void with_activation(int act, F&& f) {
+  switch (act) {
+    case kActRelu: f(std::integral_constant<int, kActRelu>{}); break;
+    case kActGelu: f(std::integral_constant<int, kActGelu>{}); break;
+    case kActGeluTanh: f(std::integral_constant<int, kActGeluTanh>{}); break;
+    case kActSilu: f(std::integral_constant<int, kActSilu>{}); break;
+    default: f(std::integral_constant<int, kActNone>{}); break;
+  }
+}
+template <typename F>
+__device__ __forceinline__ void with_flag(bool flag, F&& f) {
+  if (flag) f(std::true_type{});
+  else f(std::false_type{});
 }
 
 // Four consecutive entries of a float32 or bfloat16 array, as loaded (a bfloat16 quad fills two words):
@@ -137,7 +150,8 @@ __device__ __forceinline__ void store4(void* p, size_t at, bool bf16, bool vec, 
 // Y's value from the sum, the bias and the gate and residual as loaded
 __device__ __forceinline__ f32x4_t finish4(f32x4_t sum, f32x4_t bias, const Epilogue& ep, f32x4_t gate,
                                            f32x4_t residual) {
-  f32x4_t y = activate4(sum + bias, ep.act);
+  f32x4_t y = sum + bias;
+  with_activation(ep.act, [&](auto act) { y = activate4<decltype(act)::value>(y); });
   if (ep.gate) y *= gate;
   if (ep.residual) y += residual;
   return y;

@@ -104,89 +104,124 @@ __device__ __forceinline__ void store_tile_rows_lds(const f32x4_t (&acc)[NI][NJ]
 // stride (plain byte-addressed loads).
 constexpr int kBufferFlags = 0x00020000;
 
+// How a lane of the fused epilogue reaches gate, residual and Y, which are addressed alike: a descriptor
+// over the tile's token rows each (it drops what lies behind the last one), one lane offset (that of
+// each of its four entries where rows are not whole quads; past the descriptor's end where the row has
+// no such entry) and one uniform offset per read, which never exceeds the descriptor's size (the range
+// check subtracts it).
+struct TileRows {
+  __amdgpu_buffer_rsrc_t y, gate, residual;
+  int off[4];
+  int pitch, rows;
+};
+template <bool BF16, bool VEC>
+__device__ __forceinline__ u32x4_t load_tile4(__amdgpu_buffer_rsrc_t p, const int (&off)[4], int so) {
+  u32x4_t v = {0, 0, 0, 0};
+  if constexpr (VEC && BF16) {
+    const u32x2_t w = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_raw_buffer_load_b64(p, off[0], so, 0));
+    v[0] = w[0];
+    v[1] = w[1];
+  } else if constexpr (VEC) {
+    v = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(p, off[0], so, 0));
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if constexpr (BF16)
+        v[e / 2] |= (uint32_t)(uint16_t)__builtin_amdgcn_raw_buffer_load_b16(p, off[e], so, 0) << (16 * (e & 1));
+      else
+        v[e] = __builtin_amdgcn_raw_buffer_load_b32(p, off[e], so, 0);
+    }
+  }
+  return v;
+}
+// The uniform offset goes into the lane offset here: after a 16-byte buffer store with a scalar offset
+// register the compiler may overwrite the data registers in the next instruction, and entries of the
+// first of them were seen stored with the next value; with a constant offset it keeps the wait state.
+template <bool BF16, bool VEC, bool NT>
+__device__ __forceinline__ void store_tile4(__amdgpu_buffer_rsrc_t p, const int (&off)[4], int so, f32x4_t y) {
+  constexpr int kAux = NT ? 2 : 0;  // nt
+  if constexpr (BF16) {
+    const u32x2_t w = {round_bf16x2(y[0], y[1]), round_bf16x2(y[2], y[3])};
+    if constexpr (VEC) {
+      __builtin_amdgcn_raw_buffer_store_b64(w, p, off[0] + so, 0, kAux);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        __builtin_amdgcn_raw_buffer_store_b16((uint16_t)(w[e / 2] >> (16 * (e & 1))), p, off[e] + so, 0, 0);
+    }
+  } else if constexpr (VEC) {
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, y), p, off[0] + so, 0, kAux);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(y[e]), p, off[e] + so, 0, 0);
+  }
+}
+
+// One round of the fused epilogue, 32 tokens from `token` on: sums from the LDS buffer (`sums` at the
+// lane's first entry, READS reads TOK tokens apart), gate and residual as requested a round before,
+// those of the next round requested as soon as these are used. Activation, operands and Y's type are
+// compile-time: as branches in here they took as long as the work itself.
+template <int READS, int TOK, int PITCH, bool NT, int ACT, bool GATE, bool RESIDUAL, bool BF16, bool VEC>
+__device__ __forceinline__ void fused_round(const float* sums, f32x4_t bias, const TileRows& t, int token,
+                                            u32x4_t (&gate)[READS], u32x4_t (&residual)[READS]) {
+#pragma unroll
+  for (int k = 0; k < READS; ++k) {
+    f32x4_t y = activate4<ACT>(*(const f32x4_t*)(sums + k * TOK * PITCH) + bias);
+    if constexpr (GATE) y *= widen4(gate[k], BF16);
+    if constexpr (RESIDUAL) y += widen4(residual[k], BF16);
+    const int next = min(token + 32 + k * TOK, t.rows) * t.pitch;  // behind the last token: reads zeros
+    if constexpr (GATE) gate[k] = load_tile4<BF16, VEC>(t.gate, t.off, next);
+    if constexpr (RESIDUAL) residual[k] = load_tile4<BF16, VEC>(t.residual, t.off, next);
+    store_tile4<BF16, VEC, NT>(t.y, t.off, min(token + k * TOK, t.rows) * t.pitch, y);
+  }
+}
+
 // store_tile_rows_lds with the fused epilogue between the LDS buffer and Y: each lane finishes four
-// consecutive entries of a token row, with gate and residual read (and Y written) as whole rows. A
-// round is 32 tokens; the gate and residual entries of the next round are requested as soon as the
-// present ones are used, so their latency is paid once, not per round. The rounds run as a loop, not
-// unrolled, so that the activations' code exists once; only the reads of the accumulators, which need
-// constant indexes, are per round. Gate, residual and Y are addressed alike: a descriptor over the
-// tile's token rows (which drops what lies behind the last one), one lane offset, one uniform offset per
-// read. `row0` is the first token of the tile in Y, gate and residual.
+// consecutive entries of a token row, with gate and residual read (and Y written) as whole rows. The
+// rounds run as a loop, not unrolled, so that every form of fused_round exists once; only the reads of
+// the accumulators, which need constant indexes, are per round. `row0` is the first token of the tile in
+// Y, gate and residual.
 template <int NI, int NJ, bool NT>
 __device__ __forceinline__ void store_tile_rows_fused(const f32x4_t (&acc)[NI][NJ], float* buf, const Epilogue& ep,
                                                       size_t bias_row, void* Y, bool y_bf16, int M, int n_out,
                                                       int nrow0, int m0, size_t row0, int lane) {
   constexpr int R = 16 * NI, kPitch = R + 4, kTok = 32;
   constexpr int kLanesPerTok = R / 4, kTokPerRead = 64 / kLanesPerTok, kReads = kTok / kTokPerRead;
-  constexpr int kAux = NT ? 2 : 0;  // nt
   static_assert(NJ % 2 == 0, "32 tokens a round");
   const int q = lane >> 4, sb = lane & 15;
   const int rl = lane % kLanesPerTok, tl = lane / kLanesPerTok;
-  const int n = nrow0 + 4 * rl, left = n_out - n, rows = min(M - m0, 16 * NJ);
-  const int size = y_bf16 ? 2 : 4, pitch = n_out * size;  // n_out <= kMaxFusedOut: a tile stays below 2^31 bytes
-  const size_t first = row0 * pitch;
-  const auto descriptor = [&](const void* p) {
-    return __builtin_amdgcn_make_buffer_rsrc((void*)((const char*)p + first), (short)0, rows * pitch, kBufferFlags);
-  };
-  // every entry's own offset, past the descriptor's end where the row has no such entry
+  const int n = nrow0 + 4 * rl, left = n_out - n;
+  const int size = y_bf16 ? 2 : 4;
   const bool vec = (n_out & 3) == 0;
-  const int off = left > 0 ? tl * pitch + n * size : 0x7FFFFFFF;
-  int off1[3];
-#pragma unroll
-  for (int e = 1; e < 4; ++e) off1[e - 1] = left > e ? off + e * size : 0x7FFFFFFF;
-  const auto load = [&](__amdgpu_buffer_rsrc_t p, int so) {
-    u32x4_t v = {0, 0, 0, 0};
-    if (vec) {
-      if (y_bf16) {
-        const u32x2_t w = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_raw_buffer_load_b64(p, off, so, 0));
-        v[0] = w[0];
-        v[1] = w[1];
-      } else {
-        v = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(p, off, so, 0));
-      }
-    } else if (y_bf16) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        v[e / 2] |= (uint32_t)(uint16_t)__builtin_amdgcn_raw_buffer_load_b16(p, e ? off1[e - 1] : off, so, 0) << (16 * (e & 1));
-    } else {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = __builtin_amdgcn_raw_buffer_load_b32(p, e ? off1[e - 1] : off, so, 0);
-    }
-    return v;
+  TileRows t;
+  t.rows = min(M - m0, 16 * NJ);
+  t.pitch = n_out * size;  // n_out <= kMaxFusedOut: a tile stays below 2^31 bytes
+  const size_t first = row0 * t.pitch;
+  const auto descriptor = [&](const void* p) {
+    return __builtin_amdgcn_make_buffer_rsrc((void*)((const char*)p + first), (short)0, t.rows * t.pitch, kBufferFlags);
   };
-  const __amdgpu_buffer_rsrc_t y_rs = descriptor(Y), gate_rs = descriptor(ep.gate), res_rs = descriptor(ep.residual);
-  const auto store = [&](int so, f32x4_t y) {
-    if (y_bf16) {
-      const u32x2_t w = {round_bf16x2(y[0], y[1]), round_bf16x2(y[2], y[3])};
-      if (vec) {
-        __builtin_amdgcn_raw_buffer_store_b64(w, y_rs, off, so, kAux);
-      } else {
+  t.y = descriptor(Y);
+  t.gate = descriptor(ep.gate);
+  t.residual = descriptor(ep.residual);
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          __builtin_amdgcn_raw_buffer_store_b16((uint16_t)(w[e / 2] >> (16 * (e & 1))), y_rs, e ? off1[e - 1] : off, so, 0);
-      }
-    } else if (vec) {
-      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, y), y_rs, off, so, kAux);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(y[e]), y_rs, e ? off1[e - 1] : off, so, 0);
-    }
-  };
+  for (int e = 0; e < 4; ++e) t.off[e] = left > e ? tl * t.pitch + (n + e) * size : 0x7FFFFFFF;
   f32x4_t bias = {0, 0, 0, 0};
-  if (ep.bias && left > 0) bias = load4(ep.bias, bias_row + n, ep.bias_bf16, vec, left);
+  if (ep.bias && left > 0) bias = load4(ep.bias, bias_row + n, true, vec, left);
   u32x4_t gate[kReads], residual[kReads];
-  // (a uniform offset never exceeds the descriptor's size: the range check subtracts it)
-  const auto request = [&](int token, int k) {
-    const int so = min(token, rows) * pitch;
-    if (ep.gate) gate[k] = load(gate_rs, so);
-    if (ep.residual) residual[k] = load(res_rs, so);
-  };
+  with_flag(vec, [&](auto v) __attribute__((always_inline)) {
+    with_flag(y_bf16, [&](auto b) __attribute__((always_inline)) {
+      const auto first_round = [&](__amdgpu_buffer_rsrc_t p, u32x4_t(&to)[kReads]) __attribute__((always_inline)) {
 #pragma unroll
-  for (int k = 0; k < kReads; ++k) request(k * kTokPerRead, k);
+        for (int k = 0; k < kReads; ++k)
+          to[k] = load_tile4<decltype(b)::value, decltype(v)::value>(p, t.off, min(k * kTokPerRead, t.rows) * t.pitch);
+      };
+      if (ep.gate) first_round(t.gate, gate);
+      if (ep.residual) first_round(t.residual, residual);
+    });
+  });
 #pragma unroll 1
-  for (int c = 0; c < NJ / 2 && 32 * c < rows; ++c) {
-    static_for<NJ / 2>([&](auto cc) {
+  for (int c = 0; c < NJ / 2 && 32 * c < t.rows; ++c) {
+    static_for<NJ / 2>([&](auto cc) __attribute__((always_inline)) {
       if (c == decltype(cc)::value) {
 #pragma unroll
         for (int jj = 0; jj < 2; ++jj)
@@ -195,14 +230,20 @@ __device__ __forceinline__ void store_tile_rows_fused(const f32x4_t (&acc)[NI][N
             *(f32x4_t*)(buf + (16 * jj + sb) * kPitch + 16 * i + 4 * q) = acc[i][2 * decltype(cc)::value + jj];
       }
     });
-#pragma unroll
-    for (int k = 0; k < kReads; ++k) {
-      const int token = 32 * c + k * kTokPerRead;
-      const f32x4_t sum = *(const f32x4_t*)(buf + (k * kTokPerRead + tl) * kPitch + 4 * rl);
-      const f32x4_t y = finish4(sum, bias, ep, widen4(gate[k], y_bf16), widen4(residual[k], y_bf16));
-      request(token + 32, k);  // behind the tile's last token: reads zeros
-      store(min(token, rows) * pitch, y);
-    }
+    const float* sums = buf + tl * kPitch + 4 * rl;
+    with_flag(vec, [&](auto v) __attribute__((always_inline)) {
+      with_flag(y_bf16, [&](auto b) __attribute__((always_inline)) {
+        with_flag(ep.gate, [&](auto g) __attribute__((always_inline)) {
+          with_flag(ep.residual, [&](auto r) __attribute__((always_inline)) {
+            with_activation(ep.act, [&](auto act) __attribute__((always_inline)) {
+              fused_round<kReads, kTokPerRead, kPitch, NT, decltype(act)::value, decltype(g)::value,
+                          decltype(r)::value, decltype(b)::value, decltype(v)::value>(sums, bias, t, 32 * c, gate,
+                                                                                      residual);
+            });
+          });
+        });
+      });
+    });
   }
 }
 

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from sparse_rank_linear_prune24_amd import binding, inputs
-from tests._fused import ACTS, Weights, check, fused64, rows64
+from tests._fused import ACTS, HALF_STEP, Weights, check, fused64, rows64
 from tests._helpers import meta_to_dev, to_dev
 
 pytestmark = pytest.mark.gpu
@@ -108,6 +108,47 @@ def test_without_epilogue_is_linear_ex():
             a = run(d, "none", y, 200)
             b = binding.linear_ex(d["X"], d["values"], d["meta"], d["U"], d["V"], y_dtype=y, n_out=200)
             assert torch.equal(a, b), (M, y)
+
+
+def act64_on_device(z, act):
+    if act == "relu":
+        return z.clamp(min=0)
+    if act == "gelu":
+        return z * torch.special.ndtr(z)
+    if act == "gelu_tanh":
+        return z * torch.sigmoid(2 * (2 / torch.pi) ** 0.5 * (z + 0.044715 * z ** 3))
+    return z * torch.sigmoid(z) if act == "silu" else z
+
+
+@pytest.mark.parametrize("M,n_out", [(1280, 2048), (5000, 4096), (1000, 1030)])   # 256- and 512-row tiles, odd rows
+@pytest.mark.parametrize("y_dtype", [F32, BF16])
+def test_every_entry_of_a_large_result(M, n_out, y_dtype):
+    """The epilogue on every entry of large results, several times over, against float64 arithmetic on the
+    float32 sums (the plain product's, which the fused kernels share bit for bit)."""
+    n_in, r = 128, 16
+    g = torch.Generator(device="cuda").manual_seed(M)
+    def normal(*shape, std=1.0, to=BF16):
+        return (torch.randn(*shape, generator=g, device="cuda") * std).to(to)
+    X, U, V, bias = normal(M, n_in), normal(n_out, r, std=0.3), normal(r, n_in, std=0.3), normal(n_out)
+    values, meta = binding.prune24_pack(normal(n_out, n_in, std=0.2))
+    gate, residual = normal(M, n_out, to=y_dtype), normal(M, n_out, to=y_dtype)
+    sums = binding.linear_ex(X, values, meta, U, V, n_out=n_out).double()
+    u = 2.0 ** -24
+    for act in ACTS:
+        for b, ga, re in ((bias, gate, residual), (bias, gate, None), (None, None, residual), (bias, None, None)):
+            z = sums if b is None else sums + b.double()
+            want, bound = act64_on_device(z, act), 17 * u * z.abs()   # 16 as in tests/_fused.py, 1 for the bias sum
+            if ga is not None:
+                want, bound = want * ga.double(), bound * ga.double().abs()
+            if re is not None:
+                want = want + re.double()
+            bound = bound + 4 * u * (want.abs() + (0 if re is None else re.double().abs()))
+            bound = bound + HALF_STEP[y_dtype] * (want.abs() + bound)
+            for _ in range(3):
+                got = binding.linear_fused(X, values, meta, U, V, bias=b, activation=act, gate=ga, residual=re,
+                                           y_dtype=y_dtype, n_out=n_out)
+                wrong = int(((got.double() - want).abs() > bound).sum())
+                assert wrong == 0, (act, b is not None, ga is not None, re is not None, wrong)
 
 
 @pytest.mark.parametrize("dtype,M", [("bf16", 5), ("bf16", 130), ("fp32", 130)])
