@@ -265,9 +265,7 @@ hipError_t launch_linear_decode(const void* X, int64_t M, int64_t n_in, const vo
 }
 
 hipError_t launch_fused_decode(const FusedCall& c, int tokens, hipStream_t stream) {
-  if (tokens <= 16) return launch_fused_mb<1>(c, stream);
-  if (tokens <= 32) return launch_fused_mb<2>(c, stream);
-  return launch_fused_mb<4>(c, stream);
+  return tokens == 16 ? launch_fused_mb<1>(c, stream) : launch_fused_mb<2>(c, stream);
 }
 
 }  // namespace splr

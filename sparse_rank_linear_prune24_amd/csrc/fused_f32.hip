@@ -1,59 +1,20 @@
 // The float32 layer product with a fused epilogue, for one layer or for rows grouped by expert:
 //   Z = X S^T + (X V^T) U^T + bias,  Y = act(Z) * gate + residual     (LoSparse page, section 3.2).
 //
-// The sparse product runs on the bfloat16 structured-sparse MFMA with float32 accuracy. A float32 number
-// has 24 significant bits and a bfloat16 one 8, so x = x1 + x2 + x3 with x1 = RNE(x), x2 = RNE(x - x1),
-// x3 = x - x1 - x2, all bfloat16 and the sum exact (|x| from about 1e-30 on; below, x3 may flush). Of the
-// nine products of x1 + x2 + x3 and s1 + s2 + s3, each exact in the float32 accumulator, the six of
-// order up to 2^-16 are summed; those left out, x2 s3, x3 s2 and x3 s3, are at most 2^-23 of x s (2^-25
-// in the mean square), below the rounding of the float32 sum itself. Six structured-sparse MFMAs take
-// about 117 cycles for 16 x 16 x 64 where the float32 MFMA needs 512 on an expanded S. An infinite X
-// or S entry gives NaN (its low parts are infinity minus infinity).
-// The thin products (T = X V^T and T U^T, a few percent of the work) use the float32 MFMA.
+// Here: the first stage and the kernel for few tokens. The sparse product takes every operand as three
+// bfloat16 parts (fused_common.hpp); the thin products (T = X V^T and T U^T, a few percent of the work)
+// use the float32 MFMA.
 #include <algorithm>
 
 #include "common.hpp"
 #include "epilogue.hpp"
+#include "fused_common.hpp"
 #include "groups.hpp"
 #include "kernels.hpp"
 #include "tile_common.hpp"
 
 namespace splr {
 namespace {
-
-__device__ __forceinline__ f32x4_t mfma_f32(float a, float b, f32x4_t c) {
-  return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0);
-}
-
-// Eight float32 values as three bfloat16 parts (hardware conversion, to nearest even)
-struct Parts8 {
-  u32x4_t p[3];
-};
-__device__ __forceinline__ Parts8 split3(f32x4_t lo, f32x4_t hi) {
-  Parts8 o;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f32x2_t x = i < 2 ? f32x2_t{lo[2 * i], lo[2 * i + 1]} : f32x2_t{hi[2 * i - 4], hi[2 * i - 3]};
-#pragma unroll
-    for (int k = 0; k < 3; ++k) {
-      const uint32_t w = round_bf16x2(x[0], x[1]);
-      o.p[k][i] = w;
-      x[0] -= __uint_as_float(w << 16);
-      x[1] -= __uint_as_float(w & 0xFFFF0000u);
-    }
-  }
-  return o;
-}
-
-// acc += S . X^T over one 64-column step, S and X in parts: the small products first
-__device__ __forceinline__ f32x4_t product6(const Parts8& s, const bf16x16_t (&x)[3], int idx, f32x4_t acc) {
-  acc = smfmac16x16x64(as_bf16x8(s.p[2]), x[0], acc, idx);
-  acc = smfmac16x16x64(as_bf16x8(s.p[0]), x[2], acc, idx);
-  acc = smfmac16x16x64(as_bf16x8(s.p[1]), x[1], acc, idx);
-  acc = smfmac16x16x64(as_bf16x8(s.p[1]), x[0], acc, idx);
-  acc = smfmac16x16x64(as_bf16x8(s.p[0]), x[1], acc, idx);
-  return smfmac16x16x64(as_bf16x8(s.p[0]), x[0], acc, idx);
-}
 
 // ------------------------------------------------------------------------------- first stage
 
@@ -124,55 +85,30 @@ __global__ __launch_bounds__(256) void f32_lowrank_kernel(const float* __restric
   }
 }
 
-// acc[i][j] += U T^T over all ranks on the float32 MFMA, 16 ranks at a time: lane (sub, quad) holds ranks
-// 4 quad .. +3 of row n0 + 16 i + sub and of token m0 + 16 j + sub. T's slices are added in order.
-template <int NI, int NJ>
-__device__ __forceinline__ void add_rank_term(f32x4_t (&acc)[NI][NJ], const float* __restrict__ U,
+// acc[j] += U T^T over all ranks on the float32 MFMA, 16 ranks at a time: lane (sub, quad) holds ranks
+// 4 quad .. +3 of row n0 + sub and of token m0 + 16 j + sub. All K slices of T (kMaxSlices at most) are
+// requested together, clamped where there are fewer, and added in order.
+constexpr int kMaxSlices = 8;
+template <int NJ>
+__device__ __forceinline__ void add_rank_term(f32x4_t (&acc)[1][NJ], const float* __restrict__ U,
                                               const float* __restrict__ T, size_t slice, int slices, int M, int n_out,
                                               int r, int n0, int m0, int sub, int quad) {
   for (int j0 = 0; j0 < r; j0 += 16) {
-    f32x4_t u[NI], t[NJ];
+    const f32x4_t u = *(const f32x4_t*)(U + (size_t)min(n0 + sub, n_out - 1) * r + j0 + 4 * quad);
+    f32x4_t part[NJ][kMaxSlices];
 #pragma unroll
-    for (int i = 0; i < NI; ++i) u[i] = *(const f32x4_t*)(U + (size_t)min(n0 + 16 * i + sub, n_out - 1) * r + j0 + 4 * quad);
+    for (int j = 0; j < NJ; ++j)
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) {
-      const float* p = T + (size_t)min(m0 + 16 * j + sub, M - 1) * r + j0 + 4 * quad;
-      t[j] = *(const f32x4_t*)p;
-      for (int z = 1; z < slices; ++z) t[j] += *(const f32x4_t*)(p + z * slice);
-    }
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-#pragma unroll
-      for (int i = 0; i < NI; ++i)
-#pragma unroll
-        for (int j = 0; j < NJ; ++j) acc[i][j] = mfma_f32(u[i][e], t[j][e], acc[i][j]);
-  }
-}
-
-// Finishes and stores acc[i][j]: rows n0 + 16 i + 4 quad .. +3, token m0 + 16 j + sub (of the rows from
-// row0 on)
-template <int NI, int NJ>
-__device__ __forceinline__ void store_fragments(const f32x4_t (&acc)[NI][NJ], const Epilogue& ep, size_t bias_row,
-                                                void* Y, int y_bf16, int M, int n_out, int n0, int m0, size_t row0,
-                                                int sub, int quad) {
-#pragma unroll
-  for (int i = 0; i < NI; ++i) {
-    const int n = n0 + 16 * i + 4 * quad, left = n_out - n;
-    if (left <= 0) continue;
-    const bool vec = (n_out & 3) == 0 && left >= 4;
-    f32x4_t bias = {0, 0, 0, 0}, gate[NJ], residual[NJ];
-    if (ep.bias) bias = load4(ep.bias, bias_row + n, false, vec, left);
+      for (int z = 0; z < kMaxSlices; ++z)
+        part[j][z] = *(const f32x4_t*)(T + (size_t)min(m0 + 16 * j + sub, M - 1) * r + j0 + 4 * quad +
+                                       (z < slices ? z : 0) * slice);
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
-      const size_t at = (row0 + min(m0 + 16 * j + sub, M - 1)) * n_out + n;
-      if (ep.gate) gate[j] = load4(ep.gate, at, y_bf16, vec, left);
-      if (ep.residual) residual[j] = load4(ep.residual, at, y_bf16, vec, left);
-    }
+      f32x4_t t = part[j][0];
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) {
-      const int m = m0 + 16 * j + sub;
-      const f32x4_t y = finish4(acc[i][j], bias, ep, gate[j], residual[j]);
-      if (m < M) store4<false>(Y, (row0 + m) * n_out + n, y_bf16, vec, left, y);
+      for (int z = 1; z < kMaxSlices; ++z) t += z < slices ? part[j][z] : f32x4_t{0, 0, 0, 0};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[0][j] = mfma_f32(u[e], t[e], acc[0][j]);
     }
   }
 }
@@ -270,125 +206,8 @@ __global__ __launch_bounds__(256) void f32_decode_kernel(const float* __restrict
   for (int w = 0; w < 3; ++w)
 #pragma unroll
     for (int j = 0; j < NJ; ++j) acc[0][j] += red[(w * NJ + j) * 64 + lane];
-  add_rank_term<1, NJ>(acc, U, T, slice, slices, M, n_out, r, n0, m0, sub, quad);
+  add_rank_term<NJ>(acc, U, T, slice, slices, M, n_out, r, n0, m0, sub, quad);
   store_fragments<1, NJ>(acc, ep, e * n_out, Y, y_bf16, M, n_out, n0, m0, row0, sub, quad);
-}
-
-// ------------------------------------------------------------------------------- many tokens
-
-// Workgroup tile 64 NI rows x 64 tokens, four waves of 16 NI rows x 64 tokens. Per 64-column step X is
-// split once by the workgroup and staged in LDS as three bfloat16 planes (two buffers, one barrier a
-// step); every wave splits its own S rows in registers. Reading the planes costs each wave 24 KiB of
-// LDS per step whatever its rows, so NI = 2 (128 rows) balances LDS and the matrix cores.
-template <int NI, bool EXPERTS>
-__global__ __launch_bounds__(256) void f32_tile_kernel(const float* __restrict__ X, const float* __restrict__ values,
-                                                       const uint32_t* __restrict__ meta,
-                                                       const float* __restrict__ U, const float* __restrict__ T,
-                                                       int slices, Epilogue ep, void* Y, int y_bf16, int M, int K,
-                                                       int n_out, int r, int tiles_n, Groups groups) {
-  constexpr int NJ = 4, BM = 64, BN = 64 * NI;
-  constexpr int kPlane = BM * kXPitchU4;  // 16-byte units
-  __shared__ u32x4_t xs[2][3 * kPlane];
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int sub = lane & 15, quad = lane >> 4;
-  const int TK = (K + 63) / 64, TKB = meta_blocks(TK), TR = (n_out + 15) / 16;
-  int m_block = blockIdx.x / tiles_n;
-  const int n_block = blockIdx.x - m_block * tiles_n;
-  size_t e = 0, row0 = 0;
-  const size_t slice = (size_t)M * r;
-  if constexpr (EXPERTS) {
-    const GroupTile gt = find_group_tile<BM>(groups, m_block);
-    if (gt.expert < 0) return;
-    m_block -= gt.first;
-    M = gt.rows;
-    e = gt.expert;
-    row0 = gt.lo;
-    X += row0 * K;
-    T += row0 * r;
-    U += e * n_out * r;
-  }
-  const int m0 = m_block * BM, n0 = n_block * BN + wave * 16 * NI;
-
-  // X: thread t stages 16 columns (four lanes a row) of token row t / 4
-  const int xr = threadIdx.x >> 2, xc = (threadIdx.x & 3) * 16;
-  const float* x_src = X + (size_t)min(m0 + xr, M - 1) * K + xc;
-  f32x4_t xv[4];
-  auto load_x = [&](int kc) {
-    const bool ok = kc < TK && kc * 64 + xc < K;
-    const float* p = x_src + (ok ? kc * 64 : -xc);
-    const f32x4_t zero = {0, 0, 0, 0};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const f32x4_t v = *(const f32x4_t*)(p + 4 * i);
-      xv[i] = ok ? v : zero;
-    }
-  };
-  auto store_x = [&](int buf) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const Parts8 q = split3(xv[2 * h], xv[2 * h + 1]);
-#pragma unroll
-      for (int k = 0; k < 3; ++k) xs[buf][k * kPlane + xr * kXPitchU4 + xc / 8 + h] = q.p[k];
-    }
-  };
-  // S: the wave's row fragments (tile rows past the last repeat it; never stored)
-  const float* s_src[NI];
-  const uint16_t* m_src[NI];
-#pragma unroll
-  for (int i = 0; i < NI; ++i) {
-    const size_t tr = e * TR + min(n0 / 16 + i, TR - 1);
-    s_src[i] = values + tr * TK * 512 + lane * 8;
-    m_src[i] = (const uint16_t*)meta + (tr * TKB * 64 + lane) * 8;
-  }
-  f32x4_t sv[NI][2];
-  int idx[NI];
-  auto load_s = [&](int kc) {
-    kc = min(kc, TK - 1);
-#pragma unroll
-    for (int i = 0; i < NI; ++i) {
-      sv[i][0] = *(const f32x4_t*)(s_src[i] + (size_t)kc * 512);
-      sv[i][1] = *(const f32x4_t*)(s_src[i] + (size_t)kc * 512 + 4);
-      idx[i] = m_src[i][(size_t)(kc >> 3) * 512 + (kc & 7)];
-    }
-  };
-  f32x4_t acc[NI][NJ];
-#pragma unroll
-  for (int i = 0; i < NI; ++i)
-#pragma unroll
-    for (int j = 0; j < NJ; ++j) acc[i][j] = f32x4_t{0, 0, 0, 0};
-
-  load_x(0);
-  load_s(0);
-  store_x(0);
-  load_x(1);
-  lds_barrier();
-  for (int kc = 0; kc < TK; ++kc) {
-    const int buf = kc & 1;
-    Parts8 a[NI];
-    int nib[NI];
-#pragma unroll
-    for (int i = 0; i < NI; ++i) {
-      a[i] = split3(sv[i][0], sv[i][1]);
-      nib[i] = idx[i];
-    }
-    load_s(kc + 1);
-    store_x(buf ^ 1);  // step kc + 1; that buffer's reads ended before the last barrier
-    load_x(kc + 2);
-#pragma unroll
-    for (int j = 0; j < NJ; ++j) {
-      bf16x16_t b[3];
-#pragma unroll
-      for (int k = 0; k < 3; ++k) {
-        const int at = k * kPlane + (16 * j + sub) * kXPitchU4 + quad;
-        b[k] = cat16(as_bf16x8(xs[buf][at]), as_bf16x8(xs[buf][at + 4]));
-      }
-#pragma unroll
-      for (int i = 0; i < NI; ++i) acc[i][j] = product6(a[i], b, nib[i], acc[i][j]);
-    }
-    lds_barrier();
-  }
-  add_rank_term<NI, NJ>(acc, U, T, slice, slices, M, n_out, r, n0, m0, sub, quad);
-  store_fragments<NI, NJ>(acc, ep, e * n_out, Y, y_bf16, M, n_out, n0, m0, row0, sub, quad);
 }
 
 // ------------------------------------------------------------------------------- shapes
@@ -404,7 +223,7 @@ F32Stage1 f32_stage1(const FusedCall& c) {
   const int64_t TK = ceil_div(c.n_in, 64), others = c.r / (16 * s.rf);
   // K slices as far as they fill the chip, each at least a step for every wave; 8 at most, since every
   // workgroup of the second stage reads all of them
-  const int64_t slices = std::min<int64_t>({8, ceil_div(TK, 4), std::max<int64_t>(1, 512 / (blocks * others))});
+  const int64_t slices = std::min<int64_t>({kMaxSlices, ceil_div(TK, 4), std::max<int64_t>(1, 512 / (blocks * others))});
   s.steps_per_slice = (int)ceil_div(TK, slices);
   s.slices = (int)ceil_div(TK, s.steps_per_slice);
   s.grid = dim3((unsigned)blocks, (unsigned)others, (unsigned)s.slices);
@@ -413,51 +232,35 @@ F32Stage1 f32_stage1(const FusedCall& c) {
 
 }  // namespace
 
-int fused_f32_slices(const FusedCall& c) { return c.r > 0 ? f32_stage1(c).slices : 1; }
+int f32_lowrank_slices(const FusedCall& c) { return f32_stage1(c).slices; }
+bool f32_lowrank_grid_fits(const FusedCall& c) { return grid_fits(f32_stage1(c).grid, 256); }
 
-bool fused_f32_grids_fit(const FusedCall& c, int tokens) {
-  if (c.r > 0 && !grid_fits(f32_stage1(c).grid, 256)) return false;
-  const int64_t tile = tokens ? (tokens <= 16 ? 16 : tokens <= 32 ? 32 : 64) : 64;
-  const int64_t m = c.offsets ? most_group_tiles(c.M, c.experts, tile) : ceil_div(c.M, tile);
-  if (tokens) return m <= 65535 && grid_fits(dim3((unsigned)ceil_div(c.n_out, 16)), 256);
-  return m * ceil_div(c.n_out, 128) < (int64_t(1) << 24);
+hipError_t launch_f32_lowrank(const FusedCall& c, hipStream_t stream) {
+  const F32Stage1 s = f32_stage1(c);
+  const Groups groups{c.offsets, (int)c.experts, (int)c.M};
+  const auto launch = [&](auto kernel) {
+    kernel<<<s.grid, dim3(256), 0, stream>>>((const float*)c.X, (const float*)c.V, (int)c.M, (int)c.n_in, (int)c.r,
+                                             s.steps_per_slice, (float*)c.workspace, groups);
+  };
+  const bool experts = c.offsets != nullptr;
+  if (s.rf == 4) launch(experts ? f32_lowrank_kernel<4, true> : f32_lowrank_kernel<4, false>);
+  else if (s.rf == 2) launch(experts ? f32_lowrank_kernel<2, true> : f32_lowrank_kernel<2, false>);
+  else launch(experts ? f32_lowrank_kernel<1, true> : f32_lowrank_kernel<1, false>);
+  return hipGetLastError();
 }
 
-hipError_t launch_fused_f32(const FusedCall& c, int tokens, hipStream_t stream) {
+hipError_t launch_fused_decode_f32(const FusedCall& c, int tokens, hipStream_t stream) {
   const Groups groups{c.offsets, (int)c.experts, (int)c.M};
   const bool experts = c.offsets != nullptr;
-  if (c.r > 0) {
-    const F32Stage1 s = f32_stage1(c);
-    const auto stage1 = [&](auto kernel) {
-      kernel<<<s.grid, dim3(256), 0, stream>>>((const float*)c.X, (const float*)c.V, (int)c.M, (int)c.n_in, (int)c.r,
-                                               s.steps_per_slice, (float*)c.workspace, groups);
-    };
-    if (s.rf == 4) stage1(experts ? f32_lowrank_kernel<4, true> : f32_lowrank_kernel<4, false>);
-    else if (s.rf == 2) stage1(experts ? f32_lowrank_kernel<2, true> : f32_lowrank_kernel<2, false>);
-    else stage1(experts ? f32_lowrank_kernel<1, true> : f32_lowrank_kernel<1, false>);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-  }
-  if (tokens) {
-    const int tile = tokens <= 16 ? 16 : tokens <= 32 ? 32 : 64;
-    const dim3 grid((unsigned)ceil_div(c.n_out, 16),
-                    (unsigned)(experts ? most_group_tiles(c.M, c.experts, tile) : ceil_div(c.M, tile)));
-    const auto decode = [&](auto kernel) {
-      kernel<<<grid, dim3(256), 0, stream>>>((const float*)c.X, (const float*)c.values, c.meta, (const float*)c.U,
-                                             (const float*)c.workspace, c.slices, c.ep, c.Y, c.y_bf16 ? 1 : 0,
-                                             (int)c.M, (int)c.n_in, (int)c.n_out, (int)c.r, groups);
-    };
-    if (tile == 16) decode(experts ? f32_decode_kernel<1, 4, true> : f32_decode_kernel<1, 4, false>);
-    else if (tile == 32) decode(experts ? f32_decode_kernel<2, 2, true> : f32_decode_kernel<2, 2, false>);
-    else decode(experts ? f32_decode_kernel<4, 2, true> : f32_decode_kernel<4, 2, false>);
-    return hipGetLastError();
-  }
-  const int tiles_n = (int)ceil_div(c.n_out, 128);
-  const int64_t tiles_m = experts ? most_group_tiles(c.M, c.experts, 64) : ceil_div(c.M, 64);
-  const auto kernel = experts ? f32_tile_kernel<2, true> : f32_tile_kernel<2, false>;
-  kernel<<<dim3((unsigned)(tiles_n * tiles_m)), dim3(256), 0, stream>>>(
-      (const float*)c.X, (const float*)c.values, c.meta, (const float*)c.U, (const float*)c.workspace, c.slices, c.ep,
-      c.Y, c.y_bf16 ? 1 : 0, (int)c.M, (int)c.n_in, (int)c.n_out, (int)c.r, tiles_n, groups);
+  const dim3 grid((unsigned)ceil_div(c.n_out, 16),
+                  (unsigned)(experts ? most_group_tiles(c.M, c.experts, tokens) : ceil_div(c.M, tokens)));
+  const auto launch = [&](auto kernel) {
+    kernel<<<grid, dim3(256), 0, stream>>>((const float*)c.X, (const float*)c.values, c.meta, (const float*)c.U,
+                                           (const float*)c.workspace, c.slices, c.ep, c.Y, c.y_bf16 ? 1 : 0, (int)c.M,
+                                           (int)c.n_in, (int)c.n_out, (int)c.r, groups);
+  };
+  if (tokens == 16) launch(experts ? f32_decode_kernel<1, 4, true> : f32_decode_kernel<1, 4, false>);
+  else launch(experts ? f32_decode_kernel<2, 2, true> : f32_decode_kernel<2, 2, false>);
   return hipGetLastError();
 }
 

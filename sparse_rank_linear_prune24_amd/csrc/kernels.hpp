@@ -101,18 +101,21 @@ size_t fused_workspace_bytes(const FusedCall& c);
 // Whether every launch of the call fits the dispatch limits.
 bool fused_grids_fit(const FusedCall& c);
 hipError_t launch_fused(FusedCall c, hipStream_t stream);
-// Its parts. Stage 1 of the experts in bfloat16 and its K slices; stage 2 for many tokens a group
-// (prefill) and for few (decode, with the tokens a workgroup takes together).
+// Its parts. Stage 1 (T = X V^T in K slices): of one bfloat16 layer launch_lowrank, of bfloat16 experts and
+// of float32 layers and experts these. Stage 2: few tokens (16 or 32 a workgroup), tiles of 128 rows x 64
+// tokens, and bfloat16 tiles of 256 or 512 rows x 128 tokens.
 int experts_lowrank_slices(const FusedCall& c);
-hipError_t launch_experts_lowrank(const FusedCall& c, hipStream_t stream);
-hipError_t launch_fused_prefill(const FusedCall& c, hipStream_t stream);
-hipError_t launch_fused_decode(const FusedCall& c, int tokens, hipStream_t stream);
-// Both stages in float32 (tokens as for the decode kernel, 0: the tile kernel).
-int fused_f32_slices(const FusedCall& c);
-bool fused_f32_grids_fit(const FusedCall& c, int tokens);
-hipError_t launch_fused_f32(const FusedCall& c, int tokens, hipStream_t stream);
-bool fused_prefill_grid_fits(const FusedCall& c);
 bool experts_lowrank_grid_fits(const FusedCall& c);
+hipError_t launch_experts_lowrank(const FusedCall& c, hipStream_t stream);
+int f32_lowrank_slices(const FusedCall& c);
+bool f32_lowrank_grid_fits(const FusedCall& c);
+hipError_t launch_f32_lowrank(const FusedCall& c, hipStream_t stream);
+hipError_t launch_fused_decode(const FusedCall& c, int tokens, hipStream_t stream);
+hipError_t launch_fused_decode_f32(const FusedCall& c, int tokens, hipStream_t stream);
+bool fused_tile_grid_fits(const FusedCall& c);
+hipError_t launch_fused_tile(const FusedCall& c, hipStream_t stream);
+bool fused_prefill_grid_fits(const FusedCall& c);
+hipError_t launch_fused_prefill(const FusedCall& c, hipStream_t stream);
 
 hipError_t launch_dense_reconstruct(const void* values, const uint32_t* meta, const void* U, const void* V,
                                     int64_t n_out, int64_t n_in, int64_t r, bool bf16, float* W_hat,

@@ -92,7 +92,8 @@ struct TPairBuilder {
 #pragma unroll
       for (int u = 0; u < kGroup; ++u) sum[it] += (ok[it] && z0 + u < slices) ? v[it][u] : f32x4_t{0, 0, 0, 0};
   }
-  __device__ __forceinline__ void finish(u32x4_t* hi, u32x4_t* lo) {
+  // adds the round that was issued and the further ones
+  __device__ __forceinline__ void add_all() {
     accumulate(0);
     for (int z0 = kGroup; z0 < slices; z0 += kGroup) {
       issue(z0);
@@ -101,6 +102,18 @@ struct TPairBuilder {
       __builtin_amdgcn_sched_barrier(0);
       accumulate(z0);
     }
+  }
+  // the sums as float32, `pitch` floats a row
+  __device__ __forceinline__ void finish_sums(float* t, int pitch) {
+    add_all();
+#pragma unroll
+    for (int it = 0; it < kIters; ++it) {
+      const int q = tid + it * NT;
+      if (q < kQuads) *(f32x4_t*)(t + (q >> 4) * pitch + 4 * (q & 15)) = sum[it];
+    }
+  }
+  __device__ __forceinline__ void finish(u32x4_t* hi, u32x4_t* lo) {
+    add_all();
 #pragma unroll
     for (int it = 0; it < kIters; ++it) {
       const int q = tid + it * NT;

@@ -101,12 +101,13 @@ def test_in_place(dtype, M, y_dtype):
 
 
 def test_without_epilogue_is_linear_ex():
-    """With nothing in the epilogue the bfloat16 product is linear_ex's, bit for bit."""
-    for M in (7, 50, 200):
-        d, _, _ = case(M, 544, 200, 32, "bf16", F32, "none", False, False, False, seed=M)
+    """With nothing in the epilogue, and sizes that the same kernels take, the bfloat16 product is
+    linear_ex's, bit for bit."""
+    for M, n_out in ((7, 200), (50, 200), (2000, 4096)):
+        d, _, _ = case(M, 544, n_out, 32, "bf16", F32, "none", False, False, False, seed=M)
         for y in (F32, BF16):
-            a = run(d, "none", y, 200)
-            b = binding.linear_ex(d["X"], d["values"], d["meta"], d["U"], d["V"], y_dtype=y, n_out=200)
+            a = run(d, "none", y, n_out)
+            b = binding.linear_ex(d["X"], d["values"], d["meta"], d["U"], d["V"], y_dtype=y, n_out=n_out)
             assert torch.equal(a, b), (M, y)
 
 
@@ -120,7 +121,7 @@ def act64_on_device(z, act):
     return z * torch.sigmoid(z) if act == "silu" else z
 
 
-@pytest.mark.parametrize("M,n_out", [(1280, 2048), (5000, 4096), (1000, 1030)])   # 256- and 512-row tiles, odd rows
+@pytest.mark.parametrize("M,n_out", [(2000, 4096), (5000, 4096), (2500, 4098)])   # 256- and 512-row tiles, odd rows
 @pytest.mark.parametrize("y_dtype", [F32, BF16])
 def test_every_entry_of_a_large_result(M, n_out, y_dtype):
     """The epilogue on every entry of large results, several times over, against float64 arithmetic on the
