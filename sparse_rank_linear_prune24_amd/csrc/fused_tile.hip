@@ -54,18 +54,32 @@ __global__ __launch_bounds__(256, 2) void fused_tile_kernel(
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int sub = lane & 15, quad = lane >> 4;
   const int TK = (K + 63) / 64, TKB = meta_blocks(TK), TR = (n_out + 15) / 16;
-  int m_block = blockIdx.x / tiles_n;
-  const int n_block = blockIdx.x - m_block * tiles_n;
+  // Each XCD (own L2) runs a contiguous range of the tiles, eight token tiles at a time row block by row
+  // block, so that it reads S once for them and X once for its row blocks. Experts: all their tiles,
+  // expert after expert.
   size_t e = 0, row0 = 0;
   const int t_rows = M;
+  int tiles_m = (M + BM - 1) / BM;
+  int tile;
   if constexpr (EXPERTS) {
-    const GroupTile gt = find_group_tile<BM>(groups, m_block);
+    const int per_xcd = (group_tiles_total<BM>(groups) * tiles_n + 7) / 8;
+    if ((int)(blockIdx.x >> 3) >= per_xcd) return;
+    tile = (blockIdx.x & 7) * per_xcd + (blockIdx.x >> 3);
+    const GroupTile gt = find_group_tile<BM>(groups, tile / tiles_n);
     if (gt.expert < 0) return;
-    m_block -= gt.first;
+    tile -= gt.first * tiles_n;
+    tiles_m = gt.tiles;
     M = gt.rows;
     e = gt.expert;
     row0 = gt.lo;
+  } else {
+    tile = (blockIdx.x & 7) * (gridDim.x >> 3) + (blockIdx.x >> 3);
+    if (tile >= tiles_m * tiles_n) return;
   }
+  constexpr int kGroupM = 8;
+  const int group = tile / (kGroupM * tiles_n), in_group = tile - group * kGroupM * tiles_n;
+  const int group_m = min(kGroupM, tiles_m - group * kGroupM);
+  const int m_block = group * kGroupM + in_group % group_m, n_block = in_group / group_m;
   const int m0 = m_block * BM, n0 = n_block * BN + wave * 16 * NI;
 
   // X rows of the tile; a lane's 16 bytes of token row x_row + pass * (256 / kLanes)
@@ -238,8 +252,21 @@ __global__ __launch_bounds__(256, 2) void fused_tile_kernel(
     }
   }
   lds_barrier();
-  for (int kc = 0; kc < TK; kc += kUnroll)
-    static_for<kUnroll>([&](auto u) __attribute__((always_inline)) { step(kc + decltype(u)::value, u); });
+  if (n0 < n_out) {
+    for (int kc = 0; kc < TK; kc += kUnroll)
+      static_for<kUnroll>([&](auto u) __attribute__((always_inline)) { step(kc + decltype(u)::value, u); });
+  } else {  // a wave without rows (past the last one) only stages its share of X, with the same barriers
+    for (int kc = 0; kc < TK; kc += kUnroll)
+      static_for<kUnroll>([&](auto uu) __attribute__((always_inline)) {
+        constexpr int u = decltype(uu)::value, xq = (u + C::kLead) % PX;
+#pragma unroll
+        for (int t = 0; t < kLoads; ++t) {
+          store_x((u + C::kLead) % C::kSlots, t, xv[xq][t]);
+          load_x(kc + u + C::kLead + PX, t, xv[xq][t]);
+        }
+        if constexpr (u % C::kBarrier == C::kBarrier - 1) lds_barrier();
+      });
+  }
 
   // acc += U T^T, 64 ranks at a time: in float32 on the float32 MFMA, in bfloat16 with T as three parts, so
   // that no rank is rounded
@@ -286,7 +313,7 @@ bool fused_tile_grid_fits(const FusedCall& c) { return tile_blocks(c) * ceil_div
 
 hipError_t launch_fused_tile(const FusedCall& c, hipStream_t stream) {
   const int tiles_n = (int)ceil_div(c.n_out, 128);
-  const dim3 grid((unsigned)(tiles_n * tile_blocks(c)));
+  const dim3 grid((unsigned)(8 * ceil_div(tiles_n * tile_blocks(c), 8)));
   const Groups groups{c.offsets, (int)c.experts, (int)c.M};
   const auto launch = [&](auto f32, auto kernel) {
     using T = typename TileType<decltype(f32)::value>::T;
