@@ -1,6 +1,7 @@
 // Which kernels take a call of the layer product with a fused epilogue (splr_linear_fused,
 // splr_linear_experts).
 #include <algorithm>
+#include <cmath>
 
 #include "common.hpp"
 #include "groups.hpp"
@@ -13,16 +14,38 @@ namespace {
 // bfloat16, tiles of 256 or 512 x 128 (linear_bf16.hip).
 enum class Path { kTokens16, kTokens32, kTile, kPrefill };
 
+// The path with the least predicted time, from whole-call times on MI355X (256 CUs) over n_in 512 ..
+// 14336, n_out 1003 .. 14336, 16 .. 1024 rows and 6 .. 60 experts of 1 .. 160 rows. A workgroup costs a
+// fixed part and a part per 64-column step; workgroups run 256 at a time (the small ones of the few-token
+// kernels pack into any fraction of that); nothing is faster than reading S. Examples, bfloat16, us by path
+// (16 tokens / 32 tokens / 128 x 64 tiles / 256 x 128 tiles):
+//   4096 -> 4096    65 rows    32 /  29 /  31 /  47        256 rows     88 /  68 /  31 /  50
+//   4096 -> 14336  128 rows   150 / 115 /  33 /  50        700 rows    724 / 532 / 124 / 110
+//   1056 -> 1003   256 rows    22 /  19 /  27 /  39        700 rows     47 /  36 /  28 /  40
+//   60 experts 2048 -> 1408, 2 rows each  57 / 73 / 53 / 64;  16 rows  92 / 86 / 58 / 67;  100 rows  391 /
+//   295 / 101 / 88. float32 (three paths), 4096 -> 4096: 32 rows 37 / 31 / 74, 128 rows 106 / 86 / 76.
 Path path_of(const FusedCall& c) {
-  if (!c.offsets) {
-    if (c.M <= 16) return Path::kTokens16;
-    if (c.M <= 64) return Path::kTokens32;
-    return c.bf16 ? Path::kPrefill : Path::kTile;
-  }
-  const int64_t mean = ceil_div(c.M, c.experts);
-  if (mean <= 12) return Path::kTokens16;
-  if (mean <= 24) return Path::kTokens32;
-  return c.bf16 ? Path::kPrefill : Path::kTile;
+  const double steps = (double)ceil_div(c.n_in, 64);
+  const double active = (double)std::min(c.experts, c.M);  // experts with rows, about
+  // row blocks of all experts, each one's last about half full
+  const auto blocks = [&](int64_t rows) {
+    return c.offsets ? std::max(active, (double)c.M / rows + active / 2) : (double)ceil_div(c.M, rows);
+  };
+  const double read = active * c.n_out * c.n_in * (c.bf16 ? 1.125 : 2.125) / 4.5e6;  // S at 4.5 TB/s, us
+  const double few = (double)ceil_div(c.n_out, 16) / 256;
+  const auto few_tokens = [&](double waves, double each) { return std::max(std::max(1.0, waves) * each, read) + 6; };
+  const double t16 = few_tokens(few * blocks(16), c.bf16 ? 0.8 + 0.06 * steps : 1.0 + 0.18 * steps);
+  const double t32 = few_tokens(few * blocks(32), c.bf16 ? 1.3 + 0.1 * steps : 2.0 + 0.28 * steps);
+  const double tile_rounds = std::ceil(blocks(64) * ceil_div(c.n_out, 128) / 256);
+  const double tile = c.bf16 ? std::max(tile_rounds * (3 + 0.28 * steps) - 3, read) + 14
+                             : std::max(tile_rounds * (3 + 0.9 * steps) - 3, read) + 18;
+  const double steps16 = (double)(ceil_div(c.n_in, 1024) * 16);  // the prefill kernel runs whole rounds of 16
+  const double wide_rounds = std::ceil(blocks(128) * ceil_div(c.n_out, 256) / 256);
+  const double prefill = c.bf16 ? std::max(wide_rounds * 0.7 * steps16, read) + 14 : 1e30;
+  const double best = std::min(std::min(t16, t32), std::min(tile, prefill));
+  if (t16 == best) return Path::kTokens16;
+  if (t32 == best) return Path::kTokens32;
+  return tile == best ? Path::kTile : Path::kPrefill;
 }
 
 int slices_of(const FusedCall& c) {

@@ -92,6 +92,53 @@ def test_many_experts(E, M, dtype):
     check(run(d, offsets, "none", F32, 50, fill=-3.0), want, bound, f"{dtype} E={E} M={M}")
 
 
+# rows of 5 experts together, n_in, n_out, r: sizes that take each kernel (few tokens, 128 x 64 tiles, 256
+# and 512 x 128 tiles), quads and odd rows, more than one rank block
+LARGE = [(300, 2048, 1032, 48), (700, 1056, 1003, 80), (4000, 1024, 2048, 32), (4100, 1056, 1030, 144),
+         (26000, 512, 1024, 16)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("M,n_in,n_out,r", LARGE)
+def test_every_entry_of_large_results(M, n_in, n_out, r, dtype):
+    """Every entry of large grouped results against float64 products on the device, with the bound of
+    tests/_fused.py."""
+    dt = BF16 if dtype == "bf16" else F32
+    E, u = 5, 2.0 ** -24
+    g = torch.Generator(device="cuda").manual_seed(M)
+
+    def normal(*shape, std=1.0, to=dt):
+        return (torch.randn(*shape, generator=g, device="cuda") * std).to(to)
+    counts = [M // 5, M // 9, 0, M // 3]
+    offsets = [2]
+    for n in counts + [M - 5 - sum(counts)]:
+        offsets.append(offsets[-1] + n)
+    X, R, U, V, bias = normal(M, n_in), normal(E, n_out, n_in, std=0.05), normal(E, n_out, r, std=0.2), normal(E, r, n_in, std=0.2), normal(E, n_out)
+    packs = [binding.prune24_pack(R[e]) for e in range(E)]
+    S = [binding.dense_reconstruct(v, m, None, None, n_out=n_out, n_in=n_in).double() for v, m in packs]
+    values, meta = torch.stack([p[0] for p in packs]), torch.stack([p[1] for p in packs])
+    off = torch.tensor(offsets, dtype=torch.int32, device="cuda")
+    for y_dtype in (F32, BF16):
+        gate, residual = normal(M, n_out, to=y_dtype), normal(M, n_out, to=y_dtype)
+        out = torch.full((M, n_out), 9.0, dtype=y_dtype, device="cuda")
+        got = binding.linear_experts(X, off, values, meta, U, V, bias=bias, activation="silu", gate=gate,
+                                     residual=residual, y_dtype=y_dtype, n_out=n_out, out=out)
+        assert bool((got[:2] == 9.0).all()) and bool((got[M - 3:] == 9.0).all())
+        for e in range(E):
+            at = slice(offsets[e], offsets[e + 1])
+            x, ue, ve = X[at].double(), U[e].double(), V[e].double()
+            t = x @ ve.t()
+            z = x @ S[e].t() + t @ ue.t() + bias[e].double()
+            a = x.abs() @ S[e].abs().t() + t.abs() @ ue.abs().t() + bias[e].double().abs()
+            d = (n_in * u * (x.abs() @ ve.abs().t()) + 2.0 ** -17 * t.abs()) @ ue.abs().t() + (n_in + 2 * r + 16) * u * a
+            y, d = z * torch.sigmoid(z) * gate[at].double(), (1.13 * d + 16 * u * z.abs()) * gate[at].double().abs()
+            d = d + 4 * u * (y.abs() + residual[at].double().abs())
+            y = y + residual[at].double()
+            d = d + (u if y_dtype == F32 else 2.0 ** -8) * (y.abs() + d)
+            wrong = int(((got[at].double() - y).abs() > d).sum())
+            assert wrong == 0, (dtype, y_dtype, e, wrong)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 def test_small_integers_exactly(dtype):
     for offsets, M in GROUPS[2:]:

@@ -121,12 +121,12 @@ def act64_on_device(z, act):
     return z * torch.sigmoid(z) if act == "silu" else z
 
 
-@pytest.mark.parametrize("M,n_out", [(2000, 4096), (5000, 4096), (2500, 4098)])   # 256- and 512-row tiles, odd rows
+@pytest.mark.parametrize("M,n_out", [(2000, 4096), (4000, 4096), (8192, 4096), (2500, 4098)])
 @pytest.mark.parametrize("y_dtype", [F32, BF16])
 def test_every_entry_of_a_large_result(M, n_out, y_dtype):
     """The epilogue on every entry of large results, several times over, against float64 arithmetic on the
     float32 sums (the plain product's, which the fused kernels share bit for bit)."""
-    n_in, r = 128, 16
+    n_in, r = 1024, 16   # 256-row tiles, 512-row tiles, these with Y past the caches, rows that are no quads
     g = torch.Generator(device="cuda").manual_seed(M)
     def normal(*shape, std=1.0, to=BF16):
         return (torch.randn(*shape, generator=g, device="cuda") * std).to(to)
