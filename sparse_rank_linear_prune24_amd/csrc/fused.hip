@@ -50,14 +50,12 @@ Path path_of(const FusedCall& c) {
 
 int slices_of(const FusedCall& c) {
   if (c.r == 0) return 1;
-  if (!c.bf16) return f32_lowrank_slices(c);
-  return c.offsets ? experts_lowrank_slices(c) : lowrank_slices(c.M, c.n_in, c.r, true);
+  return c.bf16 ? fused_lowrank_slices(c) : f32_lowrank_slices(c);
 }
 
 bool stage1_fits(const FusedCall& c) {
   if (c.r == 0) return true;
-  if (!c.bf16) return f32_lowrank_grid_fits(c);
-  return c.offsets ? experts_lowrank_grid_fits(c) : lowrank_grids_fit(c.M, c.n_in, c.r, true);
+  return c.bf16 ? fused_lowrank_grid_fits(c) : f32_lowrank_grid_fits(c);
 }
 
 }  // namespace
@@ -79,9 +77,7 @@ bool fused_grids_fit(const FusedCall& c) {
 hipError_t launch_fused(FusedCall c, hipStream_t stream) {
   c.slices = slices_of(c);
   if (c.r > 0) {
-    const hipError_t e = !c.bf16    ? launch_f32_lowrank(c, stream)
-                         : c.offsets ? launch_experts_lowrank(c, stream)
-                                     : launch_lowrank(c.X, c.V, c.M, c.n_in, c.r, true, c.workspace, stream);
+    const hipError_t e = c.bf16 ? launch_fused_lowrank(c, stream) : launch_f32_lowrank(c, stream);
     if (e != hipSuccess) return e;
   }
   const Path path = path_of(c);

@@ -101,12 +101,11 @@ size_t fused_workspace_bytes(const FusedCall& c);
 // Whether every launch of the call fits the dispatch limits.
 bool fused_grids_fit(const FusedCall& c);
 hipError_t launch_fused(FusedCall c, hipStream_t stream);
-// Its parts. Stage 1 (T = X V^T in K slices): of one bfloat16 layer launch_lowrank, of bfloat16 experts and
-// of float32 layers and experts these. Stage 2: few tokens (16 or 32 a workgroup), tiles of 128 rows x 64
+// Its parts. Stage 1 (T = X V^T in K slices), in bfloat16 and in float32. Stage 2: few tokens (16 or 32 a workgroup), tiles of 128 rows x 64
 // tokens, and bfloat16 tiles of 256 or 512 rows x 128 tokens.
-int experts_lowrank_slices(const FusedCall& c);
-bool experts_lowrank_grid_fits(const FusedCall& c);
-hipError_t launch_experts_lowrank(const FusedCall& c, hipStream_t stream);
+int fused_lowrank_slices(const FusedCall& c);
+bool fused_lowrank_grid_fits(const FusedCall& c);
+hipError_t launch_fused_lowrank(const FusedCall& c, hipStream_t stream);
 int f32_lowrank_slices(const FusedCall& c);
 bool f32_lowrank_grid_fits(const FusedCall& c);
 hipError_t launch_f32_lowrank(const FusedCall& c, hipStream_t stream);

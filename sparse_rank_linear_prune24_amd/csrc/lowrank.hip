@@ -465,14 +465,28 @@ hipError_t launch_lowrank(const void* X, const void* V, int64_t M, int64_t n_in,
 
 namespace {
 
-// The experts' first stage: the shapes above, by the rows an expert has on average, with K cut into
-// slices as far as the token blocks of all experts (each expert's last one counted) leave CUs idle.
-LowrankShape experts_shape(const FusedCall& c, int64_t& blocks) {
+// The first stage of a fused call (of experts: by the rows an expert has on average, its last token block
+// counted whole). The shapes above, and for 64 ranks and many rows of one layer 64 ranks a workgroup: X is
+// read once there, where the 32-rank blocks read it twice (4096 tokens, n_in 14336: 41 -> 35 us; 2048
+// tokens, n_in 4096: 7.9 -> 7.3 us; by expert it gains nothing, since one such workgroup fills a CU's LDS
+// and the experts' odd ones cost a round). K is cut into slices as far as the token blocks leave CUs idle.
+LowrankShape fused_shape(const FusedCall& c, int64_t& blocks) {
   constexpr int64_t kWant = 256;
-  LowrankShape sh{};
   const int64_t TK = (c.n_in + 63) / 64, mean = ceil_div(c.M, c.experts);
+  const bool wide_ranks = !c.offsets && c.r == 64 && c.M >= 1024;
+  if (!c.offsets && !wide_ranks) {
+    const LowrankShape sh = lowrank_shape(c.M, c.n_in, c.r);
+    blocks = ceil_div(c.M, sh.tile ? sh.bm : 16 * sh.tf);
+    return sh;
+  }
+  LowrankShape sh{};
   int64_t per_block, others;
-  if (mean <= 16 || c.r <= 64) {
+  if (wide_ranks) {
+    sh.tf = 2;
+    sh.rf = 4;
+    per_block = 32;
+    others = 1;
+  } else if (mean <= 16 || c.r <= 64) {
     sh.tf = mean <= 16 ? 1 : 2;
     sh.rf = (mean > 16 && c.r % 32 == 0) ? 2 : 1;
     per_block = 16 * sh.tf;
@@ -483,7 +497,7 @@ LowrankShape experts_shape(const FusedCall& c, int64_t& blocks) {
     per_block = sh.bm;
     others = ceil_div(c.r, 128);
   }
-  blocks = most_group_tiles(c.M, c.experts, per_block);
+  blocks = c.offsets ? most_group_tiles(c.M, c.experts, per_block) : ceil_div(c.M, per_block);
   const int64_t most = std::min<int64_t>(mean <= 16 ? kDecodeMaxSlices : kMaxLowrankSlices, TK);
   const int64_t slices = std::min(most, std::max<int64_t>(1, ceil_div(kWant, blocks * others)));
   sh.steps_per_slice = (int)ceil_div(TK, slices);
@@ -491,28 +505,28 @@ LowrankShape experts_shape(const FusedCall& c, int64_t& blocks) {
   return sh;
 }
 
-dim3 experts_grid(const LowrankShape& sh, int64_t blocks, int64_t r) {
+dim3 fused_grid(const LowrankShape& sh, int64_t blocks, int64_t r) {
   if (sh.tile) return dim3((unsigned)(ceil_div(r, 128) * blocks), 1u, (unsigned)sh.slices);
   return dim3((unsigned)blocks, (unsigned)(r / (16 * sh.rf)), (unsigned)sh.slices);
 }
 
 }  // namespace
 
-int experts_lowrank_slices(const FusedCall& c) {
+int fused_lowrank_slices(const FusedCall& c) {
   int64_t blocks;
-  return experts_shape(c, blocks).slices;
+  return fused_shape(c, blocks).slices;
 }
 
-bool experts_lowrank_grid_fits(const FusedCall& c) {
+bool fused_lowrank_grid_fits(const FusedCall& c) {
   int64_t blocks;
-  const LowrankShape sh = experts_shape(c, blocks);
-  return grid_fits(experts_grid(sh, blocks, c.r), 256);
+  const LowrankShape sh = fused_shape(c, blocks);
+  return grid_fits(fused_grid(sh, blocks, c.r), 256);
 }
 
-hipError_t launch_experts_lowrank(const FusedCall& c, hipStream_t stream) {
+hipError_t launch_fused_lowrank(const FusedCall& c, hipStream_t stream) {
   int64_t blocks;
-  const LowrankShape sh = experts_shape(c, blocks);
-  const dim3 grid = experts_grid(sh, blocks, c.r);
+  const LowrankShape sh = fused_shape(c, blocks);
+  const dim3 grid = fused_grid(sh, blocks, c.r);
   const Groups groups{c.offsets, (int)c.experts, (int)c.M};
   const auto part = [&](auto kernel) {
     kernel<<<grid, dim3(256), 0, stream>>>((const uint16_t*)c.X, (const uint16_t*)c.V, (int)c.M, (int)c.n_in, (int)c.r,
@@ -522,20 +536,28 @@ hipError_t launch_experts_lowrank(const FusedCall& c, hipStream_t stream) {
     kernel<<<grid, dim3(256), 0, stream>>>((const uint16_t*)c.X, (const uint16_t*)c.V, (int)c.M, (int)c.n_in, (int)c.r,
                                            cdiv(c.r, 128), sh.steps_per_slice, (float*)c.workspace, groups);
   };
-  const bool deep = sh.steps_per_slice >= 16;
-  if (sh.tile) {
-    if (sh.bm == 64) tile(lowrank_tile_kernel<4, 2, 1, 4, 4, true>);
-    else tile(lowrank_tile_kernel<2, 2, 1, 4, 4, true>);
-  } else if (sh.tf == 1) {
-    if (deep) part(lowrank_bf16_kernel<1, 1, 4, 4, true>);
-    else part(lowrank_bf16_kernel<1, 1, 4, 2, true>);
-  } else if (sh.rf == 2) {
-    if (deep) part(lowrank_bf16_kernel<2, 2, 4, 4, true>);
-    else part(lowrank_bf16_kernel<2, 2, 4, 2, true>);
-  } else {
-    if (deep) part(lowrank_bf16_kernel<2, 1, 4, 4, true>);
-    else part(lowrank_bf16_kernel<2, 1, 4, 2, true>);
-  }
+  const auto launch = [&](auto mode) {
+    constexpr bool kExperts = decltype(mode)::value;
+    const bool deep = sh.steps_per_slice >= 16;
+    if (sh.tile) {
+      if (sh.bm == 64) tile(lowrank_tile_kernel<4, 2, 1, 4, 4, kExperts>);
+      else if (sh.bm == 32) tile(lowrank_tile_kernel<2, 2, 1, 4, 4, kExperts>);
+      else tile(lowrank_tile_kernel<1, 2, 1, 4, 4, kExperts>);
+    } else if (sh.tf == 1) {
+      if (deep) part(lowrank_bf16_kernel<1, 1, 4, 4, kExperts>);
+      else part(lowrank_bf16_kernel<1, 1, 4, 2, kExperts>);
+    } else if (sh.rf == 4) {
+      if constexpr (!kExperts) part(lowrank_bf16_kernel<2, 4, 4, 2>);
+    } else if (sh.rf == 2) {
+      if (deep) part(lowrank_bf16_kernel<2, 2, 4, 4, kExperts>);
+      else part(lowrank_bf16_kernel<2, 2, 4, 2, kExperts>);
+    } else {
+      if (deep) part(lowrank_bf16_kernel<2, 1, 4, 4, kExperts>);
+      else part(lowrank_bf16_kernel<2, 1, 4, 2, kExperts>);
+    }
+  };
+  if (c.offsets) launch(std::true_type{});
+  else launch(std::false_type{});
   return hipGetLastError();
 }
 
