@@ -39,9 +39,9 @@ Path path_of(const FusedCall& c) {
   const double tile_rounds = std::ceil(blocks(64) * ceil_div(c.n_out, 128) / 256);
   const double tile = c.bf16 ? std::max(tile_rounds * (3 + 0.28 * steps) - 3, read) + 14
                              : std::max(tile_rounds * (3 + 0.9 * steps) - 3, read) + 18;
-  const double steps16 = (double)(ceil_div(c.n_in, 1024) * 16);  // the prefill kernel runs whole rounds of 16
+  const double steps4 = (double)(ceil_div(c.n_in, 256) * 4);  // the prefill kernel's loop pads to four steps
   const double wide_rounds = std::ceil(blocks(128) * ceil_div(c.n_out, 256) / 256);
-  const double prefill = c.bf16 ? std::max(wide_rounds * 0.7 * steps16, read) + 14 : 1e30;
+  const double prefill = c.bf16 ? std::max(wide_rounds * 0.7 * steps4, read) + 14 : 1e30;
   const double best = std::min(std::min(t16, t32), std::min(tile, prefill));
   if (t16 == best) return Path::kTokens16;
   if (t32 == best) return Path::kTokens32;

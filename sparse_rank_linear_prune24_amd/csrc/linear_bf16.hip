@@ -699,14 +699,36 @@ linear_prefill_wide_kernel(const ModeGroup<MODE> lg, int layers, int slices, int
       bx[g] = read_b(0, g);
   });
   __builtin_amdgcn_sched_barrier(0);
-  for (int kc0 = 0; kc0 < nk_pad; kc0 += kUnroll) {
-    const int s0 = kc0 % kSlots;
-    static_for<kUnroll>([&](auto u) {
-      if constexpr (DENSE)
-        step_dense(kc0 + decltype(u)::value, s0, u);
-      else
-        step(kc0 + decltype(u)::value, s0, u);
-    });
+  if constexpr (MODE == kModePlain || NI != 2) {
+    for (int kc0 = 0; kc0 < nk_pad; kc0 += kUnroll) {
+      const int s0 = kc0 % kSlots;
+      static_for<kUnroll>([&](auto u) {
+        if constexpr (DENSE)
+          step_dense(kc0 + decltype(u)::value, s0, u);
+        else
+          step(kc0 + decltype(u)::value, s0, u);
+      });
+    }
+  } else {
+    // the same, left after every fourth step when no step is left (each fourth one ends with a barrier, as
+    // the last one does): K of any size then pads to four steps, not sixteen. Only for the 256-row tiles:
+    // with the 512-row ones' registers all in use the compiler moves accumulators across the exits.
+    static_assert(4 % kBarEvery == 0, "the loop is left behind a barrier");
+    const auto four = [&](int kc0, auto first) __attribute__((always_inline)) {
+      static_for<4>([&](auto u) {
+        step(kc0 + decltype(first)::value + decltype(u)::value, kc0 % kSlots,
+             std::integral_constant<int, decltype(first)::value + decltype(u)::value>{});
+      });
+    };
+    for (int kc0 = 0; kc0 < TK; kc0 += kUnroll) {
+      four(kc0, std::integral_constant<int, 0>{});
+      if (kc0 + 4 >= TK) break;
+      four(kc0, std::integral_constant<int, 4>{});
+      if (kc0 + 8 >= TK) break;
+      four(kc0, std::integral_constant<int, 8>{});
+      if (kc0 + 12 >= TK) break;
+      four(kc0, std::integral_constant<int, 12>{});
+    }
   }
   // ranks past the first kPreBlocks blocks, 64 at a time: T's pair in slots 0 and 1 (the last
   // step's barrier retired every LDS access of the loop), U fragments from memory
@@ -867,8 +889,11 @@ struct FusedTiles {
 FusedTiles fused_tiles(const FusedCall& c) {
   FusedTiles t;
   const int64_t likely = c.offsets ? ceil_div(c.M, 128) + std::min(c.experts, c.M) / 2 : ceil_div(c.M, 128);
-  const auto rounds = [&](int64_t bn) { return (double)ceil_div(ceil_div(c.n_out, bn) * likely, kWideMinTiles); };
-  t.bn = 1.85 * rounds(512) < rounds(256) ? 512 : 256;
+  const auto steps = [&](int64_t bn) {  // rounds of tiles times K steps as the loop pads them
+    return (double)(ceil_div(ceil_div(c.n_out, bn) * likely, kWideMinTiles) *
+                    (bn == 512 ? ceil_div(c.n_in, 1024) * 16 : ceil_div(c.n_in, 256) * 4));
+  };
+  t.bn = 1.85 * steps(512) < steps(256) ? 512 : 256;
   t.tiles_n = (int)ceil_div(c.n_out, t.bn);
   t.tiles_m = (int)(c.offsets ? most_group_tiles(c.M, c.experts, 128) : ceil_div(c.M, 128));
   t.grid = dim3((unsigned)(8 * ceil_div((int64_t)t.tiles_n * t.tiles_m, 8)));
