@@ -232,6 +232,10 @@ hipError_t launch_decode(const void* X, int64_t M, int64_t n_in, const void* val
   return hipGetLastError();
 }
 
+// The load ring is as deep as the plain product's for one layer (8 steps of 16 tokens) and 4 steps for
+// experts, whose many workgroups then fit three to a CU: 32 experts 2048 -> 1024, two rows each, 26.5 ->
+// 23.6 us (2 steps 22.3 there, but 62.6 -> 64.6 us for 4 experts 14336 -> 4096); one token 14336 -> 4096
+// prefers the deeper ring, 20.1 against 20.7 us.
 template <int MB>
 hipError_t launch_fused_mb(const FusedCall& c, hipStream_t stream) {
   constexpr int P = MB == 1 ? 8 : 4, W = 4;
@@ -244,7 +248,7 @@ hipError_t launch_fused_mb(const FusedCall& c, hipStream_t stream) {
                                               c.y_bf16 ? 1 : 0, (int)c.M, (int)c.n_in, (int)c.n_out, (int)c.r, c.ep,
                                               Groups{c.offsets, (int)c.experts, (int)c.M});
   };
-  if (experts) launch(linear_decode_kernel<MB, P, W, kModeExperts>);
+  if (experts) launch(linear_decode_kernel<MB, 4, W, kModeExperts>);
   else launch(linear_decode_kernel<MB, P, W, kModeFused>);
   return hipGetLastError();
 }

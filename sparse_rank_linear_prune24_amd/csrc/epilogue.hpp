@@ -151,7 +151,7 @@ __device__ __forceinline__ void store4(void* p, size_t at, bool bf16, bool vec, 
 __device__ __forceinline__ f32x4_t finish4(f32x4_t sum, f32x4_t bias, const Epilogue& ep, f32x4_t gate,
                                            f32x4_t residual) {
   f32x4_t y = sum + bias;
-  with_activation(ep.act, [&](auto act) { y = activate4<decltype(act)::value>(y); });
+  with_activation(ep.act, [&](auto act) __attribute__((always_inline)) { y = activate4<decltype(act)::value>(y); });
   if (ep.gate) y *= gate;
   if (ep.residual) y += residual;
   return y;
