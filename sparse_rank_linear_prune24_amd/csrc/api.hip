@@ -309,16 +309,22 @@ splr::FusedCall fused_call(const void* X, int64_t M, int64_t n_in, const int32_t
                            int64_t r, splr_dtype_t dtype, const splr::Epilogue& ep, void* Y, splr_dtype_t y_dtype,
                            void* workspace) {
   return splr::FusedCall{X, M, n_in, offsets, experts, values, meta, n_out, U, V, r, dtype == SPLR_BF16, ep, Y,
-                         y_dtype == SPLR_BF16, workspace, 1};
+                         y_dtype == SPLR_BF16, workspace};
 }
 
-size_t call_workspace_bytes(const splr::FusedCall& c) { return round_up(splr::fused_workspace_bytes(c), 256); }
+// Workspace of a call by its sizes (0 when it has no rows or does not fit the dispatch limits).
+size_t query_workspace_bytes(splr::FusedCall c) {
+  if (c.M == 0 || !splr::prepare_fused(c)) return 0;
+  return round_up(splr::fused_workspace_bytes(c), 256);
+}
 
-splr_status_t check_fused_workspace(const splr::FusedCall& c, size_t ws_bytes) {
-  const size_t need = call_workspace_bytes(c);
+// The last checks of a call with rows, then its launches.
+splr_status_t run_fused(splr::FusedCall c, size_t ws_bytes, hipStream_t stream) {
+  if (!splr::prepare_fused(c)) return SPLR_ERR_SHAPE;
+  const size_t need = round_up(splr::fused_workspace_bytes(c), 256);
   if (need > 0 && (!c.workspace || ws_bytes < need)) return SPLR_ERR_WORKSPACE;
   if (need > 0 && !aligned16(c.workspace)) return SPLR_ERR_ALIGN;
-  return SPLR_OK;
+  return from_hip(splr::launch_fused(c, stream));
 }
 
 }  // namespace
@@ -326,8 +332,10 @@ splr_status_t check_fused_workspace(const splr::FusedCall& c, size_t ws_bytes) {
 extern "C" {
 
 size_t splr_linear_fused_workspace_bytes(int64_t M, int64_t n_out, int64_t n_in, int64_t r, splr_dtype_t dtype) {
-  if (M < 1 || M > kMaxRows || check_in(n_in) != SPLR_OK || check_rank(r) != SPLR_OK || !dtype_ok(dtype)) return 0;
-  return call_workspace_bytes(fused_call(nullptr, M, n_in, nullptr, 1, nullptr, nullptr, n_out, nullptr, nullptr, r,
+  if (M < 1 || M > kMaxRows || n_out < 1 || n_out > splr::kMaxFusedOut || check_in(n_in) != SPLR_OK ||
+      check_rank(r) != SPLR_OK || !dtype_ok(dtype))
+    return 0;
+  return query_workspace_bytes(fused_call(nullptr, M, n_in, nullptr, 1, nullptr, nullptr, n_out, nullptr, nullptr, r,
                                           dtype, splr::Epilogue{}, nullptr, SPLR_FP32, nullptr));
 }
 
@@ -341,21 +349,18 @@ splr_status_t splr_linear_fused(const void* X, int64_t M, int64_t n_in, const vo
   splr::Epilogue ep;
   s = check_epilogue(epilogue, dtype, y_dtype, n_out, &ep);
   if (s != SPLR_OK) return s;
-  const splr::FusedCall c =
-      fused_call(X, M, n_in, nullptr, 1, values, meta, n_out, U, V, r, dtype, ep, Y, y_dtype, workspace);
-  if (!splr::fused_grids_fit(c)) return SPLR_ERR_SHAPE;
-  s = check_fused_workspace(c, ws_bytes);
-  if (s != SPLR_OK) return s;
-  return from_hip(splr::launch_fused(c, stream));
+  return run_fused(
+      fused_call(X, M, n_in, nullptr, 1, values, meta, n_out, U, V, r, dtype, ep, Y, y_dtype, workspace), ws_bytes,
+      stream);
 }
 
 size_t splr_linear_experts_workspace_bytes(int64_t M, int64_t n_experts, int64_t n_out, int64_t n_in, int64_t r,
                                            splr_dtype_t dtype) {
-  if (M < 0 || M > kMaxRows || n_experts < 1 || n_experts > SPLR_EXPERTS_MAX || check_in(n_in) != SPLR_OK ||
-      check_rank(r) != SPLR_OK || !dtype_ok(dtype))
+  if (M < 0 || M > kMaxRows || n_out < 1 || n_out > splr::kMaxFusedOut || n_experts < 1 ||
+      n_experts > SPLR_EXPERTS_MAX || check_in(n_in) != SPLR_OK || check_rank(r) != SPLR_OK || !dtype_ok(dtype))
     return 0;
   const int32_t any = 0;  // a non-null `offsets`: a call by expert
-  return call_workspace_bytes(fused_call(nullptr, M, n_in, &any, n_experts, nullptr, nullptr, n_out, nullptr,
+  return query_workspace_bytes(fused_call(nullptr, M, n_in, &any, n_experts, nullptr, nullptr, n_out, nullptr,
                                             nullptr, r, dtype, splr::Epilogue{}, nullptr, SPLR_FP32, nullptr));
 }
 
@@ -382,12 +387,9 @@ splr_status_t splr_linear_experts(const void* X, int64_t M, int64_t n_in, const 
       (reinterpret_cast<uintptr_t>(offsets) & 3u) || (r > 0 && (!aligned16(U) || !aligned16(V))))
     return SPLR_ERR_ALIGN;
   if (M == 0) return SPLR_OK;
-  const splr::FusedCall c =
-      fused_call(X, M, n_in, offsets, n_experts, values, meta, n_out, U, V, r, dtype, ep, Y, y_dtype, workspace);
-  if (!splr::fused_grids_fit(c)) return SPLR_ERR_SHAPE;
-  s = check_fused_workspace(c, ws_bytes);
-  if (s != SPLR_OK) return s;
-  return from_hip(splr::launch_fused(c, stream));
+  return run_fused(
+      fused_call(X, M, n_in, offsets, n_experts, values, meta, n_out, U, V, r, dtype, ep, Y, y_dtype, workspace),
+      ws_bytes, stream);
 }
 
 }  // extern "C"

@@ -10,9 +10,9 @@
 namespace splr {
 namespace {
 
-// Stage 2's kernel: few tokens (decode.hip, fused_f32.hip), tiles of 128 x 64 (fused_tile.hip), or, in
-// bfloat16, tiles of 256 or 512 x 128 (linear_bf16.hip).
-enum class Path { kTokens16, kTokens32, kTile, kPrefill };
+int64_t few_token_blocks(const FusedCall& c, int64_t tokens) {
+  return c.offsets ? most_group_tiles(c.M, c.experts, tokens) : ceil_div(c.M, tokens);
+}
 
 // The path with the least predicted time, from whole-call times on MI355X (256 CUs) over n_in 512 ..
 // 14336, n_out 1003 .. 14336, 16 .. 1024 rows and 6 .. 60 experts of 1 .. 160 rows. A workgroup costs a
@@ -24,7 +24,7 @@ enum class Path { kTokens16, kTokens32, kTile, kPrefill };
 //   1056 -> 1003   256 rows    22 /  19 /  27 /  39        700 rows     47 /  36 /  28 /  40
 //   60 experts 2048 -> 1408, 2 rows each  57 / 73 / 53 / 64;  16 rows  92 / 86 / 58 / 67;  100 rows  391 /
 //   295 / 101 / 88. float32 (three paths), 4096 -> 4096: 32 rows 37 / 31 / 74, 128 rows 106 / 86 / 76.
-Path path_of(const FusedCall& c) {
+FusedPath path_of(const FusedCall& c) {
   const double steps = (double)ceil_div(c.n_in, 64);
   const double active = (double)std::min(c.experts, c.M);  // experts with rows, about
   // row blocks of all experts, each one's last about half full
@@ -32,58 +32,46 @@ Path path_of(const FusedCall& c) {
     return c.offsets ? std::max(active, (double)c.M / rows + active / 2) : (double)ceil_div(c.M, rows);
   };
   const double read = active * c.n_out * c.n_in * (c.bf16 ? 1.125 : 2.125) / 4.5e6;  // S at 4.5 TB/s, us
-  const double few = (double)ceil_div(c.n_out, 16) / 256;
-  const auto few_tokens = [&](double waves, double each) { return std::max(std::max(1.0, waves) * each, read) + 6; };
-  const double t16 = few_tokens(few * blocks(16), c.bf16 ? 0.8 + 0.06 * steps : 1.0 + 0.18 * steps);
-  const double t32 = few_tokens(few * blocks(32), c.bf16 ? 1.3 + 0.1 * steps : 2.0 + 0.28 * steps);
+  const double never = 1e30;
+  const auto few_tokens = [&](int64_t tokens, double each) {
+    if (few_token_blocks(c, tokens) > 65535) return never;  // a grid's second dimension
+    return std::max(std::max(1.0, (double)ceil_div(c.n_out, 16) / 256 * blocks(tokens)) * each, read) + 6;
+  };
+  const double t16 = few_tokens(16, c.bf16 ? 0.8 + 0.06 * steps : 1.0 + 0.18 * steps);
+  const double t32 = few_tokens(32, c.bf16 ? 1.3 + 0.1 * steps : 2.0 + 0.28 * steps);
   const double tile_rounds = std::ceil(blocks(64) * ceil_div(c.n_out, 128) / 256);
   const double tile = c.bf16 ? std::max(tile_rounds * (3 + 0.28 * steps) - 3, read) + 14
                              : std::max(tile_rounds * (3 + 0.9 * steps) - 3, read) + 18;
   const double steps4 = (double)(ceil_div(c.n_in, 256) * 4);  // the prefill kernel's loop pads to four steps
   const double wide_rounds = std::ceil(blocks(128) * ceil_div(c.n_out, 256) / 256);
-  const double prefill = c.bf16 ? std::max(wide_rounds * 0.7 * steps4, read) + 14 : 1e30;
+  const double prefill = c.bf16 ? std::max(wide_rounds * 0.7 * steps4, read) + 14 : never;
   const double best = std::min(std::min(t16, t32), std::min(tile, prefill));
-  if (t16 == best) return Path::kTokens16;
-  if (t32 == best) return Path::kTokens32;
-  return tile == best ? Path::kTile : Path::kPrefill;
-}
-
-int slices_of(const FusedCall& c) {
-  if (c.r == 0) return 1;
-  return c.bf16 ? fused_lowrank_slices(c) : f32_lowrank_slices(c);
-}
-
-bool stage1_fits(const FusedCall& c) {
-  if (c.r == 0) return true;
-  return c.bf16 ? fused_lowrank_grid_fits(c) : f32_lowrank_grid_fits(c);
+  if (t16 == best) return FusedPath::kTokens16;
+  if (t32 == best) return FusedPath::kTokens32;
+  return tile == best ? FusedPath::kTile : FusedPath::kPrefill;
 }
 
 }  // namespace
 
-size_t fused_workspace_bytes(const FusedCall& c) {
-  return c.M == 0 || c.r == 0 ? 0 : (size_t)slices_of(c) * c.M * c.r * sizeof(float);
+bool prepare_fused(FusedCall& c) {
+  c.path = path_of(c);
+  c.slices = c.r == 0 ? 1 : c.bf16 ? fused_lowrank_slices(c) : f32_lowrank_slices(c);
+  if (c.r > 0 && !(c.bf16 ? fused_lowrank_grid_fits(c) : f32_lowrank_grid_fits(c))) return false;
+  if (c.path == FusedPath::kPrefill) return fused_prefill_grid_fits(c);
+  if (c.path == FusedPath::kTile) return fused_tile_grid_fits(c);
+  return grid_fits(dim3((unsigned)ceil_div(c.n_out, 16)), 256);
 }
 
-bool fused_grids_fit(const FusedCall& c) {
-  if (!stage1_fits(c)) return false;
-  const Path path = path_of(c);
-  if (path == Path::kPrefill) return fused_prefill_grid_fits(c);
-  if (path == Path::kTile) return fused_tile_grid_fits(c);
-  const int64_t tokens = path == Path::kTokens16 ? 16 : 32;
-  return (c.offsets ? most_group_tiles(c.M, c.experts, tokens) : ceil_div(c.M, tokens)) <= 65535 &&
-         grid_fits(dim3((unsigned)ceil_div(c.n_out, 16)), 256);
-}
+size_t fused_workspace_bytes(const FusedCall& c) { return (size_t)c.slices * c.M * c.r * sizeof(float); }
 
-hipError_t launch_fused(FusedCall c, hipStream_t stream) {
-  c.slices = slices_of(c);
+hipError_t launch_fused(const FusedCall& c, hipStream_t stream) {
   if (c.r > 0) {
     const hipError_t e = c.bf16 ? launch_fused_lowrank(c, stream) : launch_f32_lowrank(c, stream);
     if (e != hipSuccess) return e;
   }
-  const Path path = path_of(c);
-  if (path == Path::kPrefill) return launch_fused_prefill(c, stream);
-  if (path == Path::kTile) return launch_fused_tile(c, stream);
-  const int tokens = path == Path::kTokens16 ? 16 : 32;
+  if (c.path == FusedPath::kPrefill) return launch_fused_prefill(c, stream);
+  if (c.path == FusedPath::kTile) return launch_fused_tile(c, stream);
+  const int tokens = c.path == FusedPath::kTokens16 ? 16 : 32;
   return c.bf16 ? launch_fused_decode(c, tokens, stream) : launch_fused_decode_f32(c, tokens, stream);
 }
 

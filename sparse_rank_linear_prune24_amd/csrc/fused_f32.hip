@@ -85,16 +85,16 @@ __global__ __launch_bounds__(256) void f32_lowrank_kernel(const float* __restric
   }
 }
 
-// acc[j] += U T^T over all ranks on the float32 MFMA, 16 ranks at a time: lane (sub, quad) holds ranks
-// 4 quad .. +3 of row n0 + sub and of token m0 + 16 j + sub. All K slices of T (kMaxSlices at most) are
-// requested together, clamped where there are fewer, and added in order.
+// U's and T's part of 16 ranks of the rank-r term: lane (sub, quad) holds ranks j0 + 4 quad .. +3 of row
+// n0 + sub and of token m0 + 16 j + sub. All K slices of T (kMaxSlices at most) are requested together,
+// clamped where there are fewer, and added in order.
 constexpr int kMaxSlices = 8;
 template <int NJ>
-__device__ __forceinline__ void add_rank_term(f32x4_t (&acc)[1][NJ], const float* __restrict__ U,
-                                              const float* __restrict__ T, size_t slice, int slices, int M, int n_out,
-                                              int r, int n0, int m0, int sub, int quad) {
-  for (int j0 = 0; j0 < r; j0 += 16) {
-    const f32x4_t u = *(const f32x4_t*)(U + (size_t)min(n0 + sub, n_out - 1) * r + j0 + 4 * quad);
+struct Ranks16 {
+  f32x4_t u, t[NJ];
+  __device__ __forceinline__ void load(const float* __restrict__ U, const float* __restrict__ T, size_t slice,
+                                       int slices, int M, int n_out, int r, int j0, int n0, int m0, int sub, int quad) {
+    u = *(const f32x4_t*)(U + (size_t)min(n0 + sub, n_out - 1) * r + j0 + 4 * quad);
     f32x4_t part[NJ][kMaxSlices];
 #pragma unroll
     for (int j = 0; j < NJ; ++j)
@@ -104,20 +104,24 @@ __device__ __forceinline__ void add_rank_term(f32x4_t (&acc)[1][NJ], const float
                                        (z < slices ? z : 0) * slice);
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
-      f32x4_t t = part[j][0];
+      t[j] = part[j][0];
 #pragma unroll
-      for (int z = 1; z < kMaxSlices; ++z) t += z < slices ? part[j][z] : f32x4_t{0, 0, 0, 0};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) acc[0][j] = mfma_f32(u[e], t[e], acc[0][j]);
+      for (int z = 1; z < kMaxSlices; ++z) t[j] += z < slices ? part[j][z] : f32x4_t{0, 0, 0, 0};
     }
   }
-}
-
-// ------------------------------------------------------------------------------- few tokens
+  // acc[j] += U T^T on the float32 MFMA
+  __device__ __forceinline__ void add(f32x4_t (&acc)[NJ]) const {
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[j] = mfma_f32(u[e], t[j][e], acc[j]);
+  }
+};
 
 // A workgroup owns 16 rows x 16 NJ tokens; its four waves take the 64-column steps in turn, S and X
-// straight from memory P steps ahead, and are added in wave order; wave 0 finishes. Bound by reading S
-// (2.1 KiB per 16 x 64 tile) and by its latency.
+// straight from memory P steps ahead, and are added in wave order; wave 0 finishes, with the epilogue's
+// operands and the first 16 ranks of U and T requested before the loop. Bound by reading S (2.1 KiB per 16 x
+// 64 tile) and by latency.
 template <int NJ, int P, bool EXPERTS>
 __global__ __launch_bounds__(256) void f32_decode_kernel(const float* __restrict__ X, const float* __restrict__ values,
                                                          const uint32_t* __restrict__ meta,
@@ -169,10 +173,24 @@ __global__ __launch_bounds__(256) void f32_decode_kernel(const float* __restrict
       xv[u][j][3] = *(const f32x4_t*)(x + up + 4);
     }
   };
-  f32x4_t acc[1][NJ];
+  f32x4_t acc[NJ];
 #pragma unroll
-  for (int j = 0; j < NJ; ++j) acc[0][j] = f32x4_t{0, 0, 0, 0};
+  for (int j = 0; j < NJ; ++j) acc[j] = f32x4_t{0, 0, 0, 0};
+  const int n = n0 + 4 * quad, left = n_out - n;
+  const bool vec = (n_out & 3) == 0 && left >= 4;
+  f32x4_t bias = {0, 0, 0, 0}, gate[NJ], residual[NJ];
+  Ranks16<NJ> ranks;
   static_for<P>([&](auto u) { load(decltype(u)::value, decltype(u)::value); });
+  if (wave == 0) {
+    if (r > 0) ranks.load(U, T, slice, slices, M, n_out, r, 0, n0, m0, sub, quad);
+    if (ep.bias) bias = load4(ep.bias, e * n_out + n, false, vec, left);
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      const size_t at = (row0 + min(m0 + 16 * j + sub, M - 1)) * n_out + n;
+      if (ep.gate) gate[j] = load4(ep.gate, at, y_bf16, vec, left);
+      if (ep.residual) residual[j] = load4(ep.residual, at, y_bf16, vec, left);
+    }
+  }
   for (int s0 = 0; s0 < my_steps; s0 += P) {
     static_for<P>([&](auto uu) {
       constexpr int u = decltype(uu)::value;
@@ -192,22 +210,31 @@ __global__ __launch_bounds__(256) void f32_decode_kernel(const float* __restrict
       if (s0 + P < my_steps) load(s + P, u);
       if (s < my_steps) {
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) acc[0][j] = product6(a, b[j], nib, acc[0][j]);
+        for (int j = 0; j < NJ; ++j) acc[j] = product6(a, b[j], nib, acc[j]);
       }
     });
   }
   if (wave > 0) {
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) red[((wave - 1) * NJ + j) * 64 + lane] = acc[0][j];
+    for (int j = 0; j < NJ; ++j) red[((wave - 1) * NJ + j) * 64 + lane] = acc[j];
   }
   __syncthreads();
   if (wave != 0) return;
 #pragma unroll
   for (int w = 0; w < 3; ++w)
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) acc[0][j] += red[(w * NJ + j) * 64 + lane];
-  add_rank_term<NJ>(acc, U, T, slice, slices, M, n_out, r, n0, m0, sub, quad);
-  store_fragments<1, NJ>(acc, ep, e * n_out, Y, y_bf16, M, n_out, n0, m0, row0, sub, quad);
+    for (int j = 0; j < NJ; ++j) acc[j] += red[(w * NJ + j) * 64 + lane];
+  for (int j0 = 0; j0 < r; j0 += 16) {
+    if (j0 > 0) ranks.load(U, T, slice, slices, M, n_out, r, j0, n0, m0, sub, quad);
+    ranks.add(acc);
+  }
+  if (left <= 0) return;
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) {
+    const int m = m0 + 16 * j + sub;
+    const f32x4_t y = finish4(acc[j], bias, ep, gate[j], residual[j]);
+    if (m < M) store4<false>(Y, (row0 + m) * n_out + n, y_bf16, vec, left, y);
+  }
 }
 
 // ------------------------------------------------------------------------------- shapes

@@ -78,7 +78,10 @@ hipError_t launch_linear_f32(const float* X, int64_t M, int64_t n_in, const floa
 // Most outputs of a fused call: a tile's 128 token rows of float32 Y span less than 2^31 bytes.
 constexpr int64_t kMaxFusedOut = int64_t(1) << 21;
 // The layer product with a fused epilogue: splr_linear_fused (offsets NULL, one expert) and
-// splr_linear_experts. A call's operands, as its launchers take them.
+// splr_linear_experts. Stage 2's kernel: few tokens (decode.hip, fused_f32.hip), tiles of 128 x 64
+// (fused_tile.hip), or, in bfloat16, tiles of 256 or 512 x 128 (linear_bf16.hip).
+enum class FusedPath { kTokens16, kTokens32, kTile, kPrefill };
+// A call's operands, as its launchers take them.
 struct FusedCall {
   const void* X;
   int64_t M, n_in;
@@ -95,12 +98,15 @@ struct FusedCall {
   void* Y;
   bool y_bf16;
   void* workspace;  // T (fused_workspace_bytes)
-  int slices;       // K slices of T, set by launch_fused
+  // set by prepare_fused
+  int slices = 1;   // K slices of T
+  FusedPath path = FusedPath::kTokens16;
 };
+// Chooses the kernels of a call with M >= 1 rows (only the sizes and types are read); false when one of
+// its launches would exceed the dispatch limits.
+bool prepare_fused(FusedCall& c);
 size_t fused_workspace_bytes(const FusedCall& c);
-// Whether every launch of the call fits the dispatch limits.
-bool fused_grids_fit(const FusedCall& c);
-hipError_t launch_fused(FusedCall c, hipStream_t stream);
+hipError_t launch_fused(const FusedCall& c, hipStream_t stream);
 // Its parts. Stage 1 (T = X V^T in K slices), in bfloat16 and in float32. Stage 2: few tokens (16 or 32 a workgroup), tiles of 128 rows x 64
 // tokens, and bfloat16 tiles of 256 or 512 rows x 128 tokens.
 int fused_lowrank_slices(const FusedCall& c);

@@ -33,7 +33,7 @@ def test_shared_refusals(f):
         assert f(**{name: None}) == NULL, name
         assert f(**{name: MIS}) == ALIGN, name
     for kw in (dict(K=48), dict(K=0), dict(N=0), dict(M=-1), dict(r=8), dict(r=-16), dict(r=1040), dict(M=1 << 25),
-               dict(N=1 << 25), dict(K=(1 << 20) + 32)):
+               dict(N=1 << 25), dict(N=(1 << 21) + 1), dict(K=(1 << 20) + 32)):
         assert f(**kw) == SHAPE, kw
     assert f(dt=2) == DTYPE and f(yd=2) == DTYPE and f(yd=-1) == DTYPE
     for act in (-1, 5):

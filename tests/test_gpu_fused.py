@@ -39,6 +39,7 @@ def run(d, act, y_dtype, n_out, **kw):
 SHAPES = [
     (1, 32, 1, 0), (1, 4096, 96, 64), (2, 96, 17, 16), (16, 1056, 130, 48), (17, 512, 64, 128), (33, 2080, 48, 64),
     (64, 288, 1003, 32), (65, 64, 20, 16), (129, 544, 257, 80), (200, 1088, 515, 192), (300, 4096, 300, 64),
+    (9, 64, 50, 1024), (130, 96, 40, 1024),
 ]
 # act, bias, gate, residual, Y type
 EPILOGUES = [
