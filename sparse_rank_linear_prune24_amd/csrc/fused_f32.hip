@@ -121,7 +121,8 @@ struct Ranks16 {
 // A workgroup owns 16 rows x 16 NJ tokens; its four waves take the 64-column steps in turn, S and X
 // straight from memory P steps ahead, and are added in wave order; wave 0 finishes, with the epilogue's
 // operands and the first 16 ranks of U and T requested before the loop. Bound by reading S (2.1 KiB per 16 x
-// 64 tile) and by latency.
+// 64 tile) and by latency: 6.3 us for 32 tokens 512 -> 512, where two launches and four dependent loads are all
+// there is; 23 us a call for 16 tokens 4096 -> 4096 (38 MB of S and metadata).
 template <int NJ, int P, bool EXPERTS>
 __global__ __launch_bounds__(256) void f32_decode_kernel(const float* __restrict__ X, const float* __restrict__ values,
                                                          const uint32_t* __restrict__ meta,
