@@ -347,7 +347,8 @@ splr_status_t splr_linear_noalloc(const void* X, int64_t M, int64_t n_in, const 
  * Arithmetic: float32 accumulation as splr_linear; bitwise reproducible run to run.  With SPLR_FP32
  *         the sparse product runs on the bfloat16 matrix cores with every operand as the exact sum of
  *         three bfloat16 numbers; of the nine partial products the three below 2^-23 of the whole are
- *         left out.  Its error is that of a float32 sum; an infinite X or S entry gives NaN.
+ *         left out.  Its error is that of a float32 sum; an X or S entry that is infinite, or larger
+ *         than 3.39e38 in magnitude (it rounds to an infinite first part), gives NaN.
  * Errors: as splr_linear_ex; epilogue operands misaligned -> SPLR_ERR_ALIGN; activation unknown, or
  *         n_out above 2^21 -> SPLR_ERR_SHAPE.
  */

@@ -489,81 +489,89 @@ class _Epilogue(ctypes.Structure):
     _fields_ = [("activation", _I32), ("bias", _P), ("gate", _P), ("residual", _P)]
 
 
-def _is(t: torch.Tensor, dtype: torch.dtype, shape, index: int) -> bool:
-    """Whether `t` is a contiguous `dtype` tensor of `shape` on device number `index` (what `_expect`
-    checks with a message each; a serving loop's calls are mostly right, so they are asked this first)."""
-    return t.get_device() == index and t.dtype is dtype and t.shape == shape and t.is_contiguous()
-
-
 def _stream_handle(stream, index: int) -> int:
     """The HIP stream of a call on device number `index`: the given one's, or the current one's as a
-    plain number (building torch's stream object for it takes 2.7 us, a sixth of a small call)."""
+    plain number (building torch's stream object for it takes 2.7 us, a fifth of a small call)."""
     if stream is not None:
         return stream.cuda_stream
     raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
     return raw(index) if raw is not None else torch.cuda.current_stream(index).cuda_stream
 
 
-def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
-    return None if t is None else t.data_ptr()
-
-
 def _fused_call(X, offsets, values, meta, U, V, bias, activation, gate, residual, y_dtype, n_out, out, workspace,
                 stream):
     """linear_fused (offsets None) and linear_experts: checks every tensor, allocates what is missing
-    on the call's stream and calls the library. X's device is the current one."""
+    on the call's stream and calls the library, with X's device current.
+
+    Each tensor is asked in one expression whether it is contiguous, of the right type, shape and
+    device; `_expect` says what is wrong (or takes another shape of the right size) when it is not. The
+    calls of a serving loop are right, and their checks are most of what the host adds to a launch."""
     if not isinstance(X, torch.Tensor) or not _is_device(X):
         raise ValueError("X must be a device tensor")
+    index, device, dt = X.get_device(), X.device, X.dtype
+    if index >= 0 and index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return _fused_call(X, offsets, values, meta, U, V, bias, activation, gate, residual, y_dtype, n_out, out,
+                               workspace, stream)
     if X.dim() != 2 or not X.is_contiguous():
         raise ValueError(f"X must be 2-D and contiguous, got shape {tuple(X.shape)}")
     M, n_in = X.shape
-    dt, device, index = X.dtype, X.device, X.get_device()
     code = _dtype_code(X)
     if stream is not None and getattr(stream, "device", device) != device:
         raise ValueError(f"the stream belongs to {stream.device}, X to {device}")
     act = ACTIVATIONS.get(activation)
     if act is None:
         raise ValueError(f"activation must be one of {', '.join(ACTIVATIONS)}, got {activation!r}")
-    if y_dtype is torch.bfloat16:
-        ycode = SPLR_BF16
-    elif y_dtype is torch.float32:
-        ycode = SPLR_FP32
-    else:
+    if y_dtype is not torch.bfloat16 and y_dtype is not torch.float32:
         raise ValueError(f"y_dtype must be float32 or bfloat16, got {y_dtype}")
-    experts, E, lead = offsets is not None, 1, ()
+    if values is None or meta is None:
+        raise ValueError("values and meta are required")
+    if (U is None) != (V is None):
+        raise ValueError("U and V are given together (or neither, for no low-rank part)")
+    experts = offsets is not None
     if experts:
         if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1 or not 2 <= offsets.numel() <= EXPERTS_MAX + 1:
             raise ValueError(f"offsets must be a vector of 2 .. {EXPERTS_MAX + 1} entries")
         E = offsets.numel() - 1
-        lead = (E,)
-        if not _is(offsets, torch.int32, (E + 1,), index):
+        if not (offsets.dtype is torch.int32 and offsets.get_device() == index and offsets.is_contiguous()):
             _expect(offsets, "offsets", torch.int32, E + 1, device)
-    if values is None or meta is None:
-        raise ValueError("values and meta are required")
+    else:
+        E = 1
+    rank_dim = 3 if experts else 2
     if n_out is None:
-        n_out = U.shape[-2] if U is not None and U.dim() > 1 else values.shape[len(lead)] * 16
+        n_out = U.shape[-2] if U is not None and U.dim() == rank_dim else values.shape[rank_dim - 2] * 16
+    r = 0 if U is None else U.shape[-1] if U.dim() == rank_dim else -1
     TR, TK = (n_out + 15) // 16, (n_in + 63) // 64
-    if not _is(values, dt, (*lead, TR, TK, 64, 8), index):
-        _expect(values, "values", dt, E * TR * TK * 512, device)
-    if not _is(meta, torch.int32, (*lead, TR, (TK + 7) // 8, 64, 4), index):
-        _expect(meta, "meta", torch.int32, E * _meta_words(n_out, n_in), device)
-    if (U is None) != (V is None):
-        raise ValueError("U and V are given together (or neither, for no low-rank part)")
-    r = 0
-    if U is not None:
-        r = U.shape[-1] if U.dim() == 2 + len(lead) else -1
-        if not _is(U, dt, (*lead, n_out, r), index):
-            _expect(U, "U", dt, E * n_out * max(r, 0), device, (*lead, n_out, r))
-        if not _is(V, dt, (*lead, r, n_in), index):
-            _expect(V, "V", dt, E * max(r, 0) * n_in, device, (*lead, r, n_in))
-    if bias is not None and not _is(bias, dt, (*lead, n_out), index):
-        _expect(bias, "bias", dt, E * n_out, device, (*lead, n_out))
+    s_shape, m_shape, u_shape, v_shape, b_shape = ((TR, TK, 64, 8), (TR, (TK + 7) // 8, 64, 4), (n_out, r), (r, n_in),
+                                                   (n_out,))
+    if experts:
+        s_shape, m_shape, u_shape, v_shape, b_shape = (E, *s_shape), (E, *m_shape), (E, *u_shape), (E, *v_shape), (E, n_out)
     rows = (M, n_out)
-    if gate is not None and not _is(gate, y_dtype, rows, index):
-        _expect(gate, "gate", y_dtype, M * n_out, device, rows)
-    if residual is not None and not _is(residual, y_dtype, rows, index):
-        _expect(residual, "residual", y_dtype, M * n_out, device, rows)
-    L = lib()
+    if not (values.dtype is dt and values.shape == s_shape and values.get_device() == index and values.is_contiguous()):
+        _expect(values, "values", dt, E * TR * TK * 512, device)
+    if not (meta.dtype is torch.int32 and meta.shape == m_shape and meta.get_device() == index and meta.is_contiguous()):
+        _expect(meta, "meta", torch.int32, E * _meta_words(n_out, n_in), device)
+    u = v = b = g = s = ws = None   # device addresses
+    if U is not None:
+        if not (U.dtype is dt and U.shape == u_shape and U.get_device() == index and U.is_contiguous()):
+            _expect(U, "U", dt, E * n_out * max(r, 0), device, u_shape)
+        if not (V.dtype is dt and V.shape == v_shape and V.get_device() == index and V.is_contiguous()):
+            _expect(V, "V", dt, E * max(r, 0) * n_in, device, v_shape)
+        u, v = U.data_ptr(), V.data_ptr()
+    if bias is not None:
+        if not (bias.dtype is dt and bias.shape == b_shape and bias.get_device() == index and bias.is_contiguous()):
+            _expect(bias, "bias", dt, E * n_out, device, b_shape)
+        b = bias.data_ptr()
+    if gate is not None:
+        if not (gate.dtype is y_dtype and gate.shape == rows and gate.get_device() == index and gate.is_contiguous()):
+            _expect(gate, "gate", y_dtype, M * n_out, device, rows)
+        g = gate.data_ptr()
+    if residual is not None:
+        if not (residual.dtype is y_dtype and residual.shape == rows and residual.get_device() == index
+                and residual.is_contiguous()):
+            _expect(residual, "residual", y_dtype, M * n_out, device, rows)
+        s = residual.data_ptr()
+    L = _lib or lib()
     if out is None or (workspace is None and r > 0):
         with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
             if out is None:
@@ -572,30 +580,26 @@ def _fused_call(X, offsets, values, meta, U, V, bias, activation, gate, residual
                 need = (L.splr_linear_experts_workspace_bytes(M, E, n_out, n_in, r, code) if experts else
                         L.splr_linear_fused_workspace_bytes(M, n_out, n_in, r, code))
                 workspace = torch.empty(need, dtype=torch.uint8, device=device)
-    if not _is(out, y_dtype, rows, index):
+    if not (out.dtype is y_dtype and out.shape == rows and out.get_device() == index and out.is_contiguous()):
         _expect(out, "out", y_dtype, M * n_out, device, rows)
     ws_bytes = 0
     if workspace is not None:
         if not _is_device(workspace) or workspace.get_device() != index or not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous tensor on the device of X")
-        ws_bytes = workspace.nbytes
-    epilogue = _Epilogue(act, _ptr(bias), _ptr(gate), _ptr(residual))
-    layer = (values.data_ptr(), meta.data_ptr(), n_out, _ptr(U), _ptr(V), r, code, ctypes.byref(epilogue), ycode,
-             out.data_ptr(), _ptr(workspace), ws_bytes, _stream_handle(stream, index))
+        ws, ws_bytes = workspace.data_ptr(), workspace.nbytes
+    epilogue = ctypes.byref(_Epilogue(act, b, g, s))
+    ycode = SPLR_BF16 if y_dtype is torch.bfloat16 else SPLR_FP32
+    handle = _stream_handle(stream, index)
     if experts:
-        _check("splr_linear_experts",
-               L.splr_linear_experts(X.data_ptr(), M, n_in, offsets.data_ptr(), E, *layer))
+        status = L.splr_linear_experts(X.data_ptr(), M, n_in, offsets.data_ptr(), E, values.data_ptr(),
+                                       meta.data_ptr(), n_out, u, v, r, code, epilogue, ycode, out.data_ptr(), ws,
+                                       ws_bytes, handle)
     else:
-        _check("splr_linear_fused", L.splr_linear_fused(X.data_ptr(), M, n_in, *layer))
+        status = L.splr_linear_fused(X.data_ptr(), M, n_in, values.data_ptr(), meta.data_ptr(), n_out, u, v, r, code,
+                                     epilogue, ycode, out.data_ptr(), ws, ws_bytes, handle)
+    if status:
+        raise SplrError("splr_linear_experts" if experts else "splr_linear_fused", status)
     return out
-
-
-def _fused_on_device(X, *args):
-    """_fused_call with X's device current (its streams and launches belong to it)."""
-    if isinstance(X, torch.Tensor) and X.is_cuda and X.get_device() != torch.cuda.current_device():
-        with torch.cuda.device(X.device):
-            return _fused_call(X, *args)
-    return _fused_call(X, *args)
 
 
 def linear_fused(X: torch.Tensor, values: torch.Tensor, meta: torch.Tensor, U: Optional[torch.Tensor],
@@ -608,8 +612,8 @@ def linear_fused(X: torch.Tensor, values: torch.Tensor, meta: torch.Tensor, U: O
     after the products in the kernels' epilogue (splr_linear_fused). bias [n_out] of X's type; gate
     and residual [M, n_out] of y_dtype; `out` may be gate or residual itself. The workspace holds
     fused_workspace_bytes()."""
-    return _fused_on_device(X, None, values, meta, U, V, bias, activation, gate, residual, y_dtype, n_out, out,
-                            workspace, stream)
+    return _fused_call(X, None, values, meta, U, V, bias, activation, gate, residual, y_dtype, n_out, out, workspace,
+                       stream)
 
 
 def fused_workspace_bytes(M: int, n_out: int, n_in: int, r: int, dtype: torch.dtype) -> int:
@@ -637,8 +641,8 @@ def linear_experts(X: torch.Tensor, offsets: torch.Tensor, values: torch.Tensor,
     outside offsets[0] .. offsets[E]-1 of `out` are left as they were."""
     if offsets is None:
         raise ValueError("offsets is required")
-    return _fused_on_device(X, offsets, values, meta, U, V, bias, activation, gate, residual, y_dtype, n_out, out,
-                            workspace, stream)
+    return _fused_call(X, offsets, values, meta, U, V, bias, activation, gate, residual, y_dtype, n_out, out,
+                       workspace, stream)
 
 
 def dense_reconstruct(values: torch.Tensor, meta: torch.Tensor, U: Optional[torch.Tensor],
