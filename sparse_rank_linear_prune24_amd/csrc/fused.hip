@@ -35,6 +35,7 @@ FusedPath path_of(const FusedCall& c) {
   const double never = 1e30;
   const auto few_tokens = [&](int64_t tokens, double each) {
     if (few_token_blocks(c, tokens) > 65535) return never;  // a grid's second dimension
+    if (few_token_pairs(c, tokens)) each *= 0.87;
     return std::max(std::max(1.0, (double)ceil_div(c.n_out, 16) / 256 * blocks(tokens)) * each, read) + 6;
   };
   const double t16 = few_tokens(16, c.bf16 ? 0.8 + 0.06 * steps : 1.0 + 0.18 * steps);

@@ -115,6 +115,7 @@ hipError_t launch_fused_lowrank(const FusedCall& c, hipStream_t stream);
 int f32_lowrank_slices(const FusedCall& c);
 bool f32_lowrank_grid_fits(const FusedCall& c);
 hipError_t launch_f32_lowrank(const FusedCall& c, hipStream_t stream);
+bool few_token_pairs(const FusedCall& c, int64_t tokens);  // 32 rows a workgroup instead of 16
 hipError_t launch_fused_decode(const FusedCall& c, int tokens, hipStream_t stream);
 hipError_t launch_fused_decode_f32(const FusedCall& c, int tokens, hipStream_t stream);
 bool fused_tile_grid_fits(const FusedCall& c);

@@ -94,7 +94,7 @@ def test_many_experts(E, M, dtype):
 
 # rows of 5 experts together, n_in, n_out, r: sizes that take each kernel (few tokens, 128 x 64 tiles, 256
 # and 512 x 128 tiles), quads and odd rows, more than one rank block
-LARGE = [(300, 2048, 1032, 48), (700, 1056, 1003, 80), (4000, 1024, 2048, 32), (4100, 1056, 1030, 144),
+LARGE = [(64, 96, 4100, 16), (300, 2048, 1032, 48), (700, 1056, 1003, 80), (4000, 1024, 2048, 32), (4100, 1056, 1030, 144),
          (26000, 512, 1024, 16)]
 
 

@@ -40,6 +40,7 @@ SHAPES = [
     (1, 32, 1, 0), (1, 4096, 96, 64), (2, 96, 17, 16), (16, 1056, 130, 48), (17, 512, 64, 128), (33, 2080, 48, 64),
     (64, 288, 1003, 32), (65, 64, 20, 16), (129, 544, 257, 80), (200, 1088, 515, 192), (300, 4096, 300, 64),
     (9, 64, 50, 1024), (130, 96, 40, 1024),
+    (16, 96, 8200, 16), (20, 2080, 8195, 80),   # two row tiles a workgroup, an odd number of them
 ]
 # act, bias, gate, residual, Y type
 EPILOGUES = [
