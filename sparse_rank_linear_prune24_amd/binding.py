@@ -539,7 +539,12 @@ def _fused_call(X, offsets, values, meta, U, V, bias, activation, gate, residual
         E = 1
     rank_dim = 3 if experts else 2
     if n_out is None:
-        n_out = U.shape[-2] if U is not None and U.dim() == rank_dim else values.shape[rank_dim - 2] * 16
+        if U is not None and U.dim() == rank_dim:
+            n_out = U.shape[-2]
+        elif values.dim() == rank_dim + 2:
+            n_out = values.shape[rank_dim - 2] * 16
+        else:
+            raise ValueError("n_out is required when neither U's nor values' shape tells it")
     r = 0 if U is None else U.shape[-1] if U.dim() == rank_dim else -1
     TR, TK = (n_out + 15) // 16, (n_in + 63) // 64
     s_shape, m_shape, u_shape, v_shape, b_shape = ((TR, TK, 64, 8), (TR, (TK + 7) // 8, 64, 4), (n_out, r), (r, n_in),

@@ -145,3 +145,13 @@ def test_binding_rejects(host_as_device, E, bad):
 def test_experts_binding_rejects(host_as_device, bad):
     with pytest.raises((ValueError, TypeError)):
         call(3, **bad)
+
+
+@host
+@pytest.mark.parametrize("E", [None, 3])
+def test_n_out_is_asked_for_when_no_shape_tells_it(host_as_device, E):
+    flat = dict(values=layer(E)["values"].flatten(), U=None, V=None, n_out=None)
+    with pytest.raises(ValueError, match="n_out"):
+        call(E, **flat)
+    with pytest.raises(binding.SplrError, match="SPLR_ERR_HIP"):
+        call(E, **dict(flat, n_out=48))
