@@ -140,20 +140,21 @@ __device__ __forceinline__ u32x4_t load_tile4(__amdgpu_buffer_rsrc_t p, const in
 template <bool BF16, bool VEC, bool NT>
 __device__ __forceinline__ void store_tile4(__amdgpu_buffer_rsrc_t p, const int (&off)[4], int so, f32x4_t y) {
   constexpr int kAux = NT ? 2 : 0;  // nt
+  const auto at = [&](int e) __attribute__((always_inline)) { return (int)((unsigned)off[e] + (unsigned)so); };
   if constexpr (BF16) {
     const u32x2_t w = {round_bf16x2(y[0], y[1]), round_bf16x2(y[2], y[3])};
     if constexpr (VEC) {
-      __builtin_amdgcn_raw_buffer_store_b64(w, p, off[0] + so, 0, kAux);
+      __builtin_amdgcn_raw_buffer_store_b64(w, p, at(0), 0, kAux);
     } else {
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        __builtin_amdgcn_raw_buffer_store_b16((uint16_t)(w[e / 2] >> (16 * (e & 1))), p, off[e] + so, 0, 0);
+        __builtin_amdgcn_raw_buffer_store_b16((uint16_t)(w[e / 2] >> (16 * (e & 1))), p, at(e), 0, 0);
     }
   } else if constexpr (VEC) {
-    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, y), p, off[0] + so, 0, kAux);
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, y), p, at(0), 0, kAux);
   } else {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(y[e]), p, off[e] + so, 0, 0);
+    for (int e = 0; e < 4; ++e) __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(y[e]), p, at(e), 0, 0);
   }
 }
 
