@@ -335,8 +335,8 @@ splr_status_t splr_linear_noalloc(const void* X, int64_t M, int64_t n_in, const 
  * float32 and rounded once, to y_dtype, when Y is stored, so no intermediate matrix goes to memory.
  *
  *   X, values, meta, U, V, r                     as for splr_linear
- *   workspace  splr_linear_fused_workspace_bytes() bytes (0 when r == 0), clobbered; its contents on entry do not matter.  Two calls that
- *              may run at the same time need one each.
+ *   workspace  splr_linear_fused_workspace_bytes() bytes (0 when r == 0), clobbered; its contents
+ *              on entry do not matter.  Two calls that may run at the same time need one each.
  *   epilogue   NULL, or the operands below; a NULL operand is left out
  *     activation   act, applied to Z
  *     bias         [n_out] dtype, added to every row

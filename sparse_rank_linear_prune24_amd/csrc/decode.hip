@@ -1,5 +1,6 @@
 // Y = X S^T + (X V^T) U^T for few tokens (M <= 64, bfloat16; LoSparse page, §3.2): the decode
-// kernel. HBM-bound on S: a workgroup owns 16 rows; its 4 waves take interleaved 64-column K steps,
+// kernel. HBM-bound on S: a workgroup owns 16 rows (the fused forms
+// also 32, NR = 2); its 4 waves take interleaved 64-column K steps,
 // stream S straight into registers (non-temporal loads) and X through a private LDS slot each, and
 // combine their partial accumulators through LDS in a fixed order; wave 0 adds the rank-r term and
 // stores Y.
@@ -270,8 +271,8 @@ hipError_t launch_decode(const void* X, int64_t M, int64_t n_in, const void* val
   return hipGetLastError();
 }
 
-// The load ring is as deep as the plain product's for one layer (8 steps of 16 tokens) and 4 steps for
-// experts, whose many workgroups then fit three to a CU: 32 experts 2048 -> 1024, two rows each, 26.5 ->
+// The load ring is as deep as the plain product's for one layer (8 steps of 16 tokens, 4 with two
+// row tiles or 32 tokens) and 4 steps for experts, whose many workgroups then fit three to a CU: 32 experts 2048 -> 1024, two rows each, 26.5 ->
 // 23.6 us (2 steps 22.3 there, but 62.6 -> 64.6 us for 4 experts 14336 -> 4096); one token 14336 -> 4096
 // prefers the deeper ring, 20.1 against 20.7 us.
 template <int MB, int NR>
