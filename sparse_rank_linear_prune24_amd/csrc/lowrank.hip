@@ -542,7 +542,7 @@ hipError_t launch_fused_lowrank(const FusedCall& c, hipStream_t stream) {
     if (sh.tile) {
       if (sh.bm == 64) tile(lowrank_tile_kernel<4, 2, 1, 4, 4, kExperts>);
       else if (sh.bm == 32) tile(lowrank_tile_kernel<2, 2, 1, 4, 4, kExperts>);
-      else tile(lowrank_tile_kernel<1, 2, 1, 4, 4, kExperts>);
+      else if constexpr (!kExperts) tile(lowrank_tile_kernel<1, 2, 1, 4, 4>);
     } else if (sh.tf == 1) {
       if (deep) part(lowrank_bf16_kernel<1, 1, 4, 4, kExperts>);
       else part(lowrank_bf16_kernel<1, 1, 4, 2, kExperts>);
