@@ -41,7 +41,10 @@ struct URow {
 constexpr int kModePlain = 0, kModeFused = 1, kModeExperts = 2;
 
 // NR: 16-row tiles a workgroup takes (fused modes): with two, each X fragment staged serves 32 rows.
-template <int MB, int P, int WAVES, int MODE = kModePlain, int NR = 1>
+// PADDED (fused modes): some wave's steps do not fill its ring, or the last step holds 32 columns. The launcher
+// knows, so that full rings run without the tests of the last round (3 tokens 5504 -> 272: 12.5 -> 12.8 us with
+// them; 333 tokens 1056 -> 1003, where whole steps fall away, 18.4 -> 17.9).
+template <int MB, int P, int WAVES, int MODE = kModePlain, int NR = 1, bool PADDED = false>
 __global__ __launch_bounds__(64 * WAVES) void linear_decode_kernel(
     const uint16_t* __restrict__ X_, const u32x4_t* __restrict__ values_, const uint32_t* __restrict__ meta_,
     const uint16_t* __restrict__ U_, const float* __restrict__ Tpart_, int slices, void* Y, int y_bf16, int M, int K,
@@ -101,7 +104,9 @@ __global__ __launch_bounds__(64 * WAVES) void linear_decode_kernel(
   // This wave's steps are kc = wave, wave + 4, ...; a ring of P steps of loads stays in flight:
   // slot u holds step s0 + u and is refilled with step s0 + u + P as soon as it has been consumed.
   // Branch-free: steps past the wave's last one load a clamped step and contribute through a
-  // zeroed S operand.
+  // zeroed S operand. PADDED (fused modes) instead keeps an infinite X away from those zeros, whose product
+  // would be NaN where the other fused kernels read zeros: in the last round, which alone holds such
+  // steps, they are left out, and what a 32-column tail step re-reads is dropped.
   const int my_steps = (TK - wave + WAVES - 1) / WAVES;
   const int n_pad = max(1, (my_steps + P - 1) / P) * P;  // at least the final round (a wave may have no steps)
   u32x4_t sa[P][NR], xr[P][kXLoads];
@@ -164,9 +169,18 @@ __global__ __launch_bounds__(64 * WAVES) void linear_decode_kernel(
 
   auto step = [&](int s, auto uu, auto refill) {
     constexpr int u = decltype(uu)::value;
+    if constexpr (PADDED && !decltype(refill)::value) {
+      if (s >= my_steps) return;  // wave-uniform
+      if (wave + s * WAVES == TK - 1 && (K & 63) != 0 && xchunk >= 4) {
+#pragma unroll
+        for (int t = 0; t < kXLoads; ++t) xr[u][t] = u32x4_t{0, 0, 0, 0};
+      }
+    }
 #pragma unroll
     for (int t = 0; t < kXLoads; ++t) st[xdst[t]] = xr[u][t];
-    const uint32_t keep = s < my_steps ? ~0u : 0u;  // wave-uniform
+    // wave-uniform; always all ones in the fused modes, where dropping it makes the compiler's schedule
+    // slower (one token 4096 -> 4096 8.4 -> 9.0 us)
+    const uint32_t keep = s < my_steps ? ~0u : 0u;
     bf16x8_t a[NR];
     int idx[NR];
 #pragma unroll
@@ -287,8 +301,11 @@ hipError_t launch_fused_mb(const FusedCall& c, hipStream_t stream) {
                                               c.y_bf16 ? 1 : 0, (int)c.M, (int)c.n_in, (int)c.n_out, (int)c.r, c.ep,
                                               Groups{c.offsets, (int)c.experts, (int)c.M});
   };
-  if (experts) launch(linear_decode_kernel<MB, 4, W, kModeExperts, NR>);
-  else launch(linear_decode_kernel<MB, P, W, kModeFused, NR>);
+  const auto rings_full = [&](int ring) { return c.n_in % (64 * W * ring) == 0; };
+  if (experts && rings_full(4)) launch(linear_decode_kernel<MB, 4, W, kModeExperts, NR>);
+  else if (experts) launch(linear_decode_kernel<MB, 4, W, kModeExperts, NR, true>);
+  else if (rings_full(P)) launch(linear_decode_kernel<MB, P, W, kModeFused, NR>);
+  else launch(linear_decode_kernel<MB, P, W, kModeFused, NR, true>);
   return hipGetLastError();
 }
 

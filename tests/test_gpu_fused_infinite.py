@@ -1,0 +1,98 @@
+"""Infinite and not-a-number entries of X in the fused and grouped products without a rank-r part. Y's sums run
+over the entries that S keeps, so such an entry of X reaches the outputs whose row of S keeps its column, with the
+sign of what is kept there, and no other output: not through the zeros that fill S's last tile or the steps past the
+last one. The same in every kernel, whatever the number of rows selects."""
+import pytest
+import torch
+
+from sparse_rank_linear_prune24_amd import binding
+
+pytestmark = pytest.mark.gpu
+F32, BF16 = torch.float32, torch.bfloat16
+INF, NAN = float("inf"), float("nan")
+
+
+def weights(n_in, n_out, dtype, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    values, meta = binding.prune24_pack((torch.randn(n_out, n_in, generator=g, device="cuda") * 0.05).to(dtype))
+    return values, meta, binding.dense_reconstruct(values, meta, None, None, n_out=n_out, n_in=n_in).double()
+
+
+def rows(M, n_in, dtype, seed):
+    """X with one special entry a row in most rows: its first columns, its last 64 in turn, and a middle one."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    X = torch.randn(M, n_in, generator=g, device="cuda").to(dtype)
+    columns = [n_in - 32, n_in - 4, 0, n_in - 1, n_in // 2] + list(range(max(0, n_in - 64), n_in))
+    special = []
+    for m in range(M):
+        if m % 7 == 6:
+            continue   # a row without one
+        special.append((m, columns[m % len(columns)], (INF, -INF, INF, NAN)[m % 4]))
+    return X, special
+
+
+def want_of(X, S, special):
+    """(Y, bound of a float32 sum's error) in float64; special entries where S keeps their column."""
+    X = X.double()
+    want, bound = X @ S.t(), (X.shape[1] + 16) * 2.0 ** -24 * (X.abs() @ S.abs().t())
+    for m, k, v in special:
+        s = S[:, k]
+        assert bool((s != 0).any()) and bool((s == 0).any())
+        want[m] = torch.where(s == 0, want[m] - X[m, k] * s, v * torch.sign(s))
+    return want, bound
+
+
+def check(got, want, bound, tag):
+    got = got.double()
+    finite = torch.isfinite(want)
+    wrong = int(((got - want).abs() > bound)[finite].sum()) + int((~torch.isfinite(got))[finite].sum())
+    other = ~((got == want) | (torch.isnan(got) & torch.isnan(want)))
+    wrong_special = int(other[~finite].sum())
+    print(f"[infinite] {tag}: {wrong} finite and {wrong_special} other entries wrong", flush=True)
+    assert wrong == 0 and wrong_special == 0, tag
+
+
+# M, n_in, n_out: the few-token kernels (16 and 32 tokens, one and two row tiles), 128 x 64 tiles, 256- and 512-row
+# tiles; n_in that is 0 and 32 mod 64, and steps that leave the waves' rings part-filled
+SINGLE = [(1, 96, 40), (5, 64, 40), (16, 4128, 50), (12, 2112, 130), (16, 96, 8200), (9, 160, 8195), (40, 1056, 1003), (64, 544, 70),
+          (20, 2080, 8195), (32, 2112, 8200), (256, 4096, 4096), (250, 4128, 4090), (2000, 1056, 4096),
+          (2000, 1024, 4096), (4000, 1056, 4096), (4000, 960, 4098)]
+TYPES = [BF16]
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("M,n_in,n_out", SINGLE)
+def test_one_layer(M, n_in, n_out, dtype):
+    print(f"[infinite] {M} x {n_in} -> {n_out} {dtype}", flush=True)
+    values, meta, S = weights(n_in, n_out, dtype, seed=M)
+    for turn in range(4 if M == 1 else 1):
+        X, special = rows(M, n_in, dtype, seed=M + turn)
+        if M == 1:
+            special = [(0, [n_in - 32, n_in - 4, 0, n_in - 1][turn], INF)]
+        want, bound = want_of(X, S, special)
+        for m, k, v in special:
+            X[m, k] = v
+        check(binding.linear_fused(X, values, meta, None, None, n_out=n_out), want, bound, f"{M} {n_in} {n_out} {dtype}")
+
+
+# rows of 4 experts together, n_in, n_out
+GROUPED = [(8, 96, 40), (30, 2080, 1000), (64, 96, 4100), (300, 2080, 1032), (700, 1056, 1003), (4000, 1056, 2048),
+           (26000, 544, 1024)]
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("M,n_in,n_out", GROUPED)
+def test_experts(M, n_in, n_out, dtype):
+    print(f"[infinite] experts {M} x {n_in} -> {n_out} {dtype}", flush=True)
+    ends = [0, M // 3, M // 3, M // 2, M]
+    layers = [weights(n_in, n_out, dtype, seed=M + e) for e in range(4)]
+    X, special = rows(M, n_in, dtype, seed=M)
+    want, bound = torch.empty(M, n_out, dtype=torch.float64, device="cuda"), torch.empty(M, n_out, dtype=torch.float64, device="cuda")
+    for e in range(4):
+        lo, hi = ends[e], ends[e + 1]
+        want[lo:hi], bound[lo:hi] = want_of(X[lo:hi], layers[e][2], [(m - lo, k, v) for m, k, v in special if lo <= m < hi])
+    for m, k, v in special:
+        X[m, k] = v
+    got = binding.linear_experts(X, torch.tensor(ends, dtype=torch.int32, device="cuda"), torch.stack([l[0] for l in layers]),
+                                 torch.stack([l[1] for l in layers]), None, None, n_out=n_out)
+    check(got, want, bound, f"experts {M} {n_in} {n_out} {dtype}")
