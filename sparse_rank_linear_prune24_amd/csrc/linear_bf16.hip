@@ -284,16 +284,21 @@ __device__ __forceinline__ u32x4_t expand_groups(uint32_t k0, uint32_t k1, uint3
 }
 
 // Wait states between accumulator writes by ordinary instructions and smfmac_acc (or the reverse),
-// followed by an empty asm per accumulator that every later use depends on, so the compiler cannot
-// move an accumulator read or write across the wait states (64 > the pass count of the 16x16x64
-// structured-sparse MFMA and every write-to-read distance the matrix core needs).
+// between two empty asms per accumulator on which every earlier and later use depends, so the compiler
+// cannot move an accumulator read or write (a zero that it copies into each one included) across the wait states
+// (64 > the pass count of the 16x16x64 structured-sparse MFMA and every write-to-read distance the
+// matrix core needs).
 template <int NI, int NJ>
 __device__ __forceinline__ void accumulator_fence(f32x4_t (&acc)[NI][NJ]) {
+  const auto pin = [&]() __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) asm volatile("" : "+a"(acc[i][j]));
+  };
+  pin();
   asm volatile("s_nop 15\n\ts_nop 15\n\ts_nop 15\n\ts_nop 15" ::: "memory");
-#pragma unroll
-  for (int i = 0; i < NI; ++i)
-#pragma unroll
-    for (int j = 0; j < NJ; ++j) asm volatile("" : "+a"(acc[i][j]));
+  pin();
 }
 
 // Operand fences: the registers passed through one were last written before it (vector-ALU
@@ -761,11 +766,21 @@ linear_prefill_wide_kernel(const ModeGroup<MODE> lg, int layers, int slices, int
     }
   }
   // ranks past the first kPreBlocks blocks, 64 at a time: T's pair in slots 0 and 1 (the last
-  // step's barrier retired every LDS access of the loop), U fragments from memory
+  // step's barrier retired every LDS access of the loop), U fragments from memory. The fused modes' 512-row
+  // tiles have no register to spare here, and with T's loads four slices at a time the compiler moved all
+  // accumulators aside between the MFMAs. So T comes two slices at a time and U's fragments after it, which moves
+  // nothing, and fences keep it harmless should it move some again (500 rows 960 -> 32768, 192 ranks: 82 -> 76 us).
   for (int j0 = r_pre; j0 < r; j0 += 64) {
     UFragments<NI> uf;
-    uf.load(U, n_out, r, j0, nrow0, lane);
-    build_t_pair<BM, 64 * WAVES>(Tpart, slices, M, r, m0, j0, xs, xs + kSlot, threadIdx.x, t_rows);
+    if constexpr (MODE == kModePlain) {
+      uf.load(U, n_out, r, j0, nrow0, lane);
+      build_t_pair<BM, 64 * WAVES>(Tpart, slices, M, r, m0, j0, xs, xs + kSlot, threadIdx.x, t_rows);
+    } else {
+      accumulator_fence(acc);
+      build_t_pair<BM, 64 * WAVES, 2>(Tpart, slices, M, r, m0, j0, xs, xs + kSlot, threadIdx.x, t_rows);
+      uf.load(U, n_out, r, j0, nrow0, lane);
+      accumulator_fence(acc);
+    }
     lds_barrier();
     lowrank_block_acc<NI, NJ>(acc, uf, xs, xs + kSlot);
     lds_barrier();

@@ -131,10 +131,10 @@ struct TPairBuilder {
   }
 };
 
-template <int ROWS, int NT>
+template <int ROWS, int NT, int G = 0>
 __device__ __forceinline__ void build_t_pair(const float* __restrict__ Tpart, int slices, int M, int r, int m0,
                                              int j0, u32x4_t* hi, u32x4_t* lo, int tid, int t_rows = 0) {
-  TPairBuilder<ROWS, NT> tb;
+  TPairBuilder<ROWS, NT, G> tb;
   tb.init(Tpart, slices, M, r, m0, j0, tid, t_rows);
   tb.issue(0);
   __builtin_amdgcn_sched_barrier(0);
