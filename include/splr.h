@@ -344,15 +344,16 @@ splr_status_t splr_linear_noalloc(const void* X, int64_t M, int64_t n_in, const 
  *     residual     [M][n_out] y_dtype, added last
  *   Y          [M][n_out] y_dtype.  It may be the very buffer of gate or of residual (same address:
  *              every entry is read before it is written); it must not overlap anything else.
- * Arithmetic: float32 accumulation as splr_linear; bitwise reproducible run to run.  The sparse sums
- *         run over the entries that S keeps: with SPLR_BF16 an infinite or NaN entry of X reaches
- *         the outputs whose row of S keeps its column and no others (with r > 0 the whole row of Y is
- *         NaN, as X V^T then passes as two bfloat16 numbers, infinity minus infinity the second).
- *         With SPLR_FP32
+ * Arithmetic: float32 accumulation as splr_linear; bitwise reproducible run to run.  With SPLR_FP32
  *         the sparse product runs on the bfloat16 matrix cores with every operand as the exact sum of
- *         three bfloat16 numbers; of the nine partial products the three below 2^-23 of the whole are
- *         left out.  Its error is that of a float32 sum; an X or S entry that is infinite, or larger
- *         than 3.39e38 in magnitude (it rounds to an infinite first part), gives NaN.
+ *         three bfloat16 numbers (entries below 2^-110 in magnitude are off by up to 2^-134); of the
+ *         nine partial products the three below 2^-23 of the whole are left out.  Its error is that of
+ *         a float32 sum.
+ *         The sparse sums run over the entries that S keeps: an infinite or NaN entry of X reaches the
+ *         outputs whose row of S keeps its column and no others.  (SPLR_FP32 forms sums that come out
+ *         NaN a second time, one by one: rows with such entries take longer.)  With r > 0 and SPLR_BF16
+ *         it makes the whole row of Y NaN, as X V^T then passes as several bfloat16 numbers, infinity
+ *         minus infinity among them.
  * Errors: as splr_linear_ex; epilogue operands misaligned -> SPLR_ERR_ALIGN; activation unknown, or
  *         n_out above 2^21 -> SPLR_ERR_SHAPE.
  */

@@ -3,12 +3,14 @@
 //
 // In float32 the sparse product runs on the bfloat16 structured-sparse MFMA with float32 accuracy. A float32 number
 // has 24 significant bits and a bfloat16 one 8, so x = x1 + x2 + x3 with x1 = RNE(x), x2 = RNE(x - x1),
-// x3 = x - x1 - x2, all bfloat16 and the sum exact (|x| from about 1e-30 on; below, x3 may flush). Of the
+// x3 = x - x1 - x2, all bfloat16 and the sum exact (|x| from 2^-110 on; below, x3 is rounded to a multiple
+// of 2^-133, bfloat16's least number, which the conversions and the MFMA keep). Of the
 // nine products of x1 + x2 + x3 and s1 + s2 + s3, each exact in the float32 accumulator, the six of
 // order up to 2^-16 are summed; those left out, x2 s3, x3 s2 and x3 s3, are at most 2^-23 of x s (2^-25
 // in the mean square), below the rounding of the float32 sum itself. Six structured-sparse MFMAs take
-// about 117 cycles for 16 x 16 x 64 where the float32 MFMA needs 512 on an expanded S. An infinite X
-// or S entry gives NaN (its low parts are infinity minus infinity).
+// about 117 cycles for 16 x 16 x 64 where the float32 MFMA needs 512 on an expanded S. An infinite X or S
+// entry, or one above 3.39e38 (x1 rounds to infinity), makes its sums NaN, since the low parts are infinity
+// minus infinity: sums that end as NaN are formed once more, in float32 (resum_nan).
 #pragma once
 
 #include "common.hpp"
@@ -60,6 +62,57 @@ __device__ __forceinline__ f32x4_t product6(const Parts8& s, const bf16x16_t (&x
   acc = smfmac16x16x64(as_bf16x8(s.p[1]), x[0], acc, idx);
   acc = smfmac16x16x64(as_bf16x8(s.p[0]), x[1], acc, idx);
   return smfmac16x16x64(as_bf16x8(s.p[0]), x[0], acc, idx);
+}
+
+// Row `row` of a tile row of S (its values and metadata from their first tile column on) times x, over the kept
+// entries in order
+__device__ __forceinline__ float sparse_dot(const float* __restrict__ x, const float* __restrict__ values,
+                                            const uint32_t* __restrict__ meta, int row, int K) {
+  float sum = 0.0f;
+#pragma unroll 4
+  for (int g = 0; g < K / 4; ++g) {
+    const int tk = g / 16, lane = row + 16 * (g % 16 / 4);
+    const uint32_t nib = meta_unit(meta, 0, 0, tk, lane) >> (4 * (g % 4));
+    const float* kept = values + (size_t)tk * 512 + lane * 8 + 2 * (g % 4);
+    sum = fmaf(x[4 * g + (nib & 3u)], kept[0], sum);
+    sum = fmaf(x[4 * g + ((nib >> 2) & 3u)], kept[1], sum);
+  }
+  return sum;
+}
+
+// Forms those of the sums acc[i][j] that are NaN again, so that operands which the bfloat16 parts cannot carry give
+// what float32 gives. Layout as store_fragments; values and meta: S of the tile row of n0, TK and TKB its
+// blocks a tile row. Without such sums this is half a comparison for each (0 to 0.3 us a call); with
+// them the wave takes as long for each as a lane of the plain float32 product.
+template <int NI, int NJ>
+__device__ __forceinline__ void resum_nan(f32x4_t (&acc)[NI][NJ], const float* __restrict__ X,
+                                          const float* __restrict__ values, const uint32_t* __restrict__ meta, int K,
+                                          int M, int n_out, int n0, int m0, int sub, int quad) {
+  const auto any_nan = [](f32x4_t v) { return __builtin_isunordered(v[0], v[1]) || __builtin_isunordered(v[2], v[3]); };
+  bool nan = false;
+#pragma unroll
+  for (int i = 0; i < NI; ++i)
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) nan |= any_nan(acc[i][j]);
+  if (__builtin_expect(!__any(nan), 1)) return;
+  const int TK = (K + 63) / 64, TKB = meta_blocks(TK);
+#pragma unroll
+  for (int i = 0; i < NI; ++i)
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      const int m = m0 + 16 * j + sub, n = n0 + 16 * i + 4 * quad;
+      const f32x4_t v = acc[i][j];
+      if (!any_nan(v)) continue;
+#pragma unroll 1
+      for (int e = 0; e < 4; ++e) {
+        const float old = e == 0 ? v[0] : e == 1 ? v[1] : e == 2 ? v[2] : v[3];
+        if (old == old || m >= M || n + e >= n_out) continue;
+        const float sum = sparse_dot(X + (size_t)m * K, values + (size_t)i * TK * 512, meta + (size_t)i * TKB * 256,
+                                     4 * quad + e, K);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) acc[i][j][k] = e == k ? sum : acc[i][j][k];
+      }
+    }
 }
 
 // Finishes and stores acc[i][j]: rows n0 + 16 i + 4 quad .. +3, token m0 + 16 j + sub (of the rows from

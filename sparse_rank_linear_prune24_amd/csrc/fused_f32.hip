@@ -225,6 +225,8 @@ __global__ __launch_bounds__(256) void f32_decode_kernel(const float* __restrict
   for (int w = 0; w < 3; ++w)
 #pragma unroll
     for (int j = 0; j < NJ; ++j) acc[j] += red[(w * NJ + j) * 64 + lane];
+  resum_nan<1, NJ>(reinterpret_cast<f32x4_t(&)[1][NJ]>(acc), X, values + tr * TK * 512, meta + tr * TKB * 256, K, M, n_out,
+                   n0, m0, sub, quad);
   for (int j0 = 0; j0 < r; j0 += 16) {
     if (j0 > 0) ranks.load(U, T, slice, slices, M, n_out, r, j0, n0, m0, sub, quad);
     ranks.add(acc);

@@ -277,6 +277,12 @@ __global__ __launch_bounds__(256, 2) void fused_tile_kernel(
       });
   }
 
+  if constexpr (F32) {
+    if (n0 < n_out)
+      resum_nan(acc, X + row0 * K, values + (e * TR + n0 / 16) * (size_t)TK * 512,
+                meta + (e * TR + n0 / 16) * (size_t)TKB * 256, K, M, n_out, n0, m0, sub, quad);
+  }
+
   // acc += U T^T, 64 ranks at a time: in float32 on the float32 MFMA, in bfloat16 with T as three parts, so
   // that no rank is rounded
   for (int j0 = 0; j0 < r; j0 += 64) {

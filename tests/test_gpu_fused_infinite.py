@@ -1,7 +1,8 @@
 """Infinite and not-a-number entries of X in the fused and grouped products without a rank-r part. Y's sums run
 over the entries that S keeps, so such an entry of X reaches the outputs whose row of S keeps its column, with the
 sign of what is kept there, and no other output: not through the zeros that fill S's last tile or the steps past the
-last one. The same in every kernel, whatever the number of rows selects."""
+last one. The same in every kernel, whatever the number of rows selects. In float32 too, where the kernels multiply
+bfloat16 parts: there finite entries above bfloat16's range, and S's own infinities, give what float32 gives."""
 import pytest
 import torch
 
@@ -10,6 +11,7 @@ from sparse_rank_linear_prune24_amd import binding
 pytestmark = pytest.mark.gpu
 F32, BF16 = torch.float32, torch.bfloat16
 INF, NAN = float("inf"), float("nan")
+LARGE = 3.4e38   # finite in float32, infinite in bfloat16
 
 
 def weights(n_in, n_out, dtype, seed):
@@ -28,16 +30,23 @@ def rows(M, n_in, dtype, seed):
         if m % 7 == 6:
             continue   # a row without one
         special.append((m, columns[m % len(columns)], (INF, -INF, INF, NAN)[m % 4]))
+        if dtype == F32 and m % 5 == 4:
+            special[-1] = (*special[-1][:2], LARGE if m % 2 else -LARGE)
     return X, special
 
 
 def want_of(X, S, special):
     """(Y, bound of a float32 sum's error) in float64; special entries where S keeps their column."""
     X = X.double()
+    for m, k, v in special:
+        if abs(v) == LARGE:
+            X[m, k] = v
     want, bound = X @ S.t(), (X.shape[1] + 16) * 2.0 ** -24 * (X.abs() @ S.abs().t())
     for m, k, v in special:
         s = S[:, k]
         assert bool((s != 0).any()) and bool((s == 0).any())
+        if abs(v) == LARGE:
+            continue
         want[m] = torch.where(s == 0, want[m] - X[m, k] * s, v * torch.sign(s))
     return want, bound
 
@@ -57,7 +66,7 @@ def check(got, want, bound, tag):
 SINGLE = [(1, 96, 40), (5, 64, 40), (16, 4128, 50), (12, 2112, 130), (16, 96, 8200), (9, 160, 8195), (40, 1056, 1003), (64, 544, 70),
           (20, 2080, 8195), (32, 2112, 8200), (256, 4096, 4096), (250, 4128, 4090), (2000, 1056, 4096),
           (2000, 1024, 4096), (4000, 1056, 4096), (4000, 960, 4098)]
-TYPES = [BF16]
+TYPES = [BF16, F32]
 
 
 @pytest.mark.parametrize("dtype", TYPES)
@@ -96,3 +105,64 @@ def test_experts(M, n_in, n_out, dtype):
     got = binding.linear_experts(X, torch.tensor(ends, dtype=torch.int32, device="cuda"), torch.stack([l[0] for l in layers]),
                                  torch.stack([l[1] for l in layers]), None, None, n_out=n_out)
     check(got, want, bound, f"experts {M} {n_in} {n_out} {dtype}")
+
+
+# n_in, n_out, rows of X: few tokens, tiles, and in bfloat16 the prefill kernels
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("M,n_in,n_out", [(3, 96, 40), (40, 1056, 500), (256, 2080, 4100), (2000, 1056, 4096)])
+def test_infinite_weights(M, n_in, n_out, dtype):
+    """An infinite entry of S makes its output infinite with the sign of X there, and no other output."""
+    g = torch.Generator(device="cuda").manual_seed(M)
+    R = (torch.randn(n_out, n_in, generator=g, device="cuda") * 0.05).to(dtype)
+    at = [(n, (7 * n) % n_in, INF if n % 2 else -INF) for n in range(1, n_out, 9)] + [(n_out - 1, n_in - 1, INF)]
+    for n, k, v in at:
+        R[n, k] = v   # the largest of its group: kept
+    values, meta = binding.prune24_pack(R)
+    for n, k, v in at:
+        R[n, k] = 0.0
+    others = torch.ones(n_out, dtype=torch.bool, device="cuda")
+    others[[n for n, _, _ in at]] = False
+    S = binding.dense_reconstruct(*binding.prune24_pack(R), None, None, n_out=n_out, n_in=n_in).double()
+    X = torch.randn(M, n_in, generator=g, device="cuda").to(dtype)
+    X = torch.where(X == 0, torch.ones_like(X), X)
+    got = binding.linear_fused(X, values, meta, None, None, n_out=n_out).double()
+    for n, k, v in at:
+        assert bool((got[:, n] == v * torch.sign(X[:, k].double())).all()), n
+    want, bound = X.double() @ S.t(), (n_in + 16) * 2.0 ** -24 * (X.double().abs() @ S.abs().t())
+    assert bool(((got - want).abs() <= bound)[:, others].all())
+
+
+@pytest.mark.parametrize("M,n_in,n_out", [(3, 96, 40), (40, 1056, 500), (300, 2080, 1030)])
+def test_infinity_through_the_factors(M, n_in, n_out):
+    """float32 with ranks: positive weights and factors carry a positive infinity to the whole row, and only there."""
+    g = torch.Generator(device="cuda").manual_seed(M)
+
+    def positive(*shape):
+        return torch.rand(*shape, generator=g, device="cuda") + 0.1
+    values, meta = binding.prune24_pack(positive(n_out, n_in))
+    U, V, X = positive(n_out, 48), positive(48, n_in), positive(M, n_in)
+    clean = binding.linear_fused(X, values, meta, U, V, n_out=n_out)
+    bad = list(range(0, M, 2))
+    for m in bad:
+        X[m, (5 * m + n_in - 1) % n_in] = INF
+    got = binding.linear_fused(X, values, meta, U, V, n_out=n_out)
+    assert bool((got[bad] == INF).all())
+    assert torch.equal(got[1::2], clean[1::2])
+
+
+@pytest.mark.parametrize("scale", [-126, -120, -112, -104])
+@pytest.mark.parametrize("M,n_in,n_out", [(3, 96, 40), (300, 2080, 1030)])
+def test_tiny_entries(M, n_in, n_out, scale):
+    """float32 entries so small that their low parts leave bfloat16's range: its subnormal numbers are 2^-133 apart, so
+    an entry is off by 2^-134 at most (2^-133 counted here) and its product by that times the other factor; a product's
+    own rounding among float32's subnormal numbers is 2^-150."""
+    values, meta, S = weights(n_in, n_out, F32, seed=M)
+    values, S = values * 2.0 ** 20, S * 2.0 ** 20
+    g = torch.Generator(device="cuda").manual_seed(M)
+    X = torch.randn(M, n_in, generator=g, device="cuda", dtype=torch.float64).mul(2.0 ** scale).float()
+    got = binding.linear_fused(X, values, meta, None, None, n_out=n_out).double()
+    x = X.double()
+    want, s = x @ S.t(), S.abs().sum(1)[None]
+    bound = (n_in + 16) * 2.0 ** -24 * (x.abs() @ S.abs().t()) + 2.0 ** -133 * (s + x.abs().sum(1)[:, None]) + 6 * n_in * 2.0 ** -150
+    print(f"[infinite] 2^{scale}: error / bound {float(((got - want).abs() / bound).max()):.3g}", flush=True)
+    assert bool(((got - want).abs() <= bound).all())
