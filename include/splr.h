@@ -335,8 +335,8 @@ splr_status_t splr_linear_noalloc(const void* X, int64_t M, int64_t n_in, const 
  * float32 and rounded once, to y_dtype, when Y is stored, so no intermediate matrix goes to memory.
  *
  *   X, values, meta, U, V, r                     as for splr_linear
- *   workspace  splr_linear_fused_workspace_bytes() bytes (0 when r == 0), clobbered; its contents
- *              on entry do not matter.  Two calls that may run at the same time need one each.
+ *   workspace  splr_linear_fused_workspace_bytes() bytes (0 when r == 0, and for sizes that the call
+ *              refuses), clobbered; its contents on entry do not matter.  Two calls that may run at the same time need one each.
  *   epilogue   NULL, or the operands below; a NULL operand is left out
  *     activation   act, applied to Z
  *     bias         [n_out] dtype, added to every row
@@ -392,8 +392,8 @@ splr_status_t splr_linear_fused(const void* X, int64_t M, int64_t n_in, const vo
  *   U [n_experts][n_out][r], V [n_experts][r][n_in] dtype (NULL iff r == 0)
  *   epilogue   as splr_linear_fused, bias [n_experts][n_out]
  *   Y          as splr_linear_fused
- *   workspace  splr_linear_experts_workspace_bytes() bytes (0 when r == 0), clobbered; its contents
- *              on entry do not matter.  Two calls that may run at the same time need one each.
+ *   workspace  splr_linear_experts_workspace_bytes() bytes (0 when r == 0, when M == 0, and for sizes
+ *              that the call refuses), clobbered; its contents on entry do not matter.  Two calls that may run at the same time need one each.
  * M may be 0 (no row was routed here): nothing is enqueued and X, gate, residual and Y may be NULL.
  * Arithmetic: as splr_linear_fused; a row's result depends on its own row and its expert only,
  * except for the order of the float32 sums, which follows the kernel that M and n_experts select.

@@ -41,11 +41,14 @@ FusedPath path_of(const FusedCall& c) {
   const double t16 = few_tokens(16, c.bf16 ? 0.8 + 0.06 * steps : 1.0 + 0.18 * steps);
   const double t32 = few_tokens(32, c.bf16 ? 1.3 + 0.1 * steps : 2.0 + 0.28 * steps);
   const double tile_rounds = std::ceil(blocks(64) * ceil_div(c.n_out, 128) / 256);
-  const double tile = c.bf16 ? std::max(tile_rounds * (3 + 0.28 * steps) - 3, read) + 14
-                             : std::max(tile_rounds * (3 + 0.9 * steps) - 3, read) + 18;
+  // a launch that the dispatch limits do not take is no choice. One path always fits: with the tiles past the
+  // limits n_out is 2^20 or more, so there are few rows, and the few-token kernels take these
+  const double tile = !fused_tile_grid_fits(c) ? never
+                      : c.bf16 ? std::max(tile_rounds * (3 + 0.28 * steps) - 3, read) + 14
+                               : std::max(tile_rounds * (3 + 0.9 * steps) - 3, read) + 18;
   const double steps4 = (double)(ceil_div(c.n_in, 256) * 4);  // the prefill kernel's loop pads to four steps
   const double wide_rounds = std::ceil(blocks(128) * ceil_div(c.n_out, 256) / 256);
-  const double prefill = c.bf16 ? std::max(wide_rounds * 0.7 * steps4, read) + 14 : never;
+  const double prefill = c.bf16 && fused_prefill_grid_fits(c) ? std::max(wide_rounds * 0.7 * steps4, read) + 14 : never;
   const double best = std::min(std::min(t16, t32), std::min(tile, prefill));
   if (t16 == best) return FusedPath::kTokens16;
   if (t32 == best) return FusedPath::kTokens32;

@@ -73,6 +73,18 @@ def test_workspace_sizes():
             assert need >= M * r * 4 and fused(M=M, K=K, r=r, dt=dt, wsb=need - 1) == WORKSPACE
 
 
+# experts, n_in, n_out, rows: inside every documented limit, with more tiles than a launch of the tile kernels takes
+@pytest.mark.parametrize("dt", [0, 1])
+@pytest.mark.parametrize("E,K,N,M", [(1024, 64, 1 << 20, 1500), (1024, 64, 1 << 20, 8000), (1024, 32, (1 << 21) - 7, 1024), (512, 64, 1 << 21, 600),
+                                     (512, 64, 1 << 21, 4000), (256, 128, 1 << 21, 32768), (700, 32, 3 << 19, 16000),
+                                     (1000, 32, 1 << 21, 32768)])
+def test_the_largest_sizes_find_a_kernel(E, K, N, M, dt):
+    for r in (16, 64, 128):
+        need = binding.lib().splr_linear_experts_workspace_bytes(M, E, N, K, r, dt)
+        assert need >= M * r * 4
+        assert experts(M=M, K=K, E=E, N=N, r=r, dt=dt, wsb=need - 1) == WORKSPACE
+
+
 # ----------------------------------------------------------------------------- the binding
 class _Stream:
     cuda_stream = 0

@@ -85,3 +85,22 @@ def test_outputs_repeat(M, dtype):
                                bias=bias.repeat(times), gate=gate.repeat(1, times))
     assert int((want != 0).sum()) > want.numel() // 3
     assert torch.equal(got.view(M, times, block), want[:, None].expand(-1, times, -1))
+
+
+def test_more_tiles_than_a_launch_takes():
+    """512 experts of 2^21 outputs: the tile kernels' grids would pass the dispatch limits, so the few-token kernel runs.
+    Every expert has the same S, and its rows repeat."""
+    E, n_in, block, times, M = 512, 64, 256, 2 ** 13, 600
+    print(f"[large] {E} experts {M} rows {n_in} -> {block * times}", flush=True)
+    torch.cuda.empty_cache()
+    v, m, _, _, bias = layer(n_in, block, 16, BF16, seed=5)
+    values = torch.empty((E * times, *v.shape), dtype=v.dtype, device="cuda").copy_(v).view(E, times * v.shape[0], *v.shape[1:])
+    meta = torch.empty((E * times, *m.shape), dtype=m.dtype, device="cuda").copy_(m).view(E, times * m.shape[0], *m.shape[1:])
+    X = ternary(M, n_in, to=BF16, seed=1)
+    ends = torch.linspace(0, M, E + 1).int().cuda()
+    got = binding.linear_experts(X, ends, values, meta, None, None, bias=bias.repeat(E, times), y_dtype=BF16)
+    want = binding.linear_fused(X, v, m, None, None, bias=bias, y_dtype=BF16)
+    assert int((want != 0).sum()) > want.numel() // 3
+    assert torch.equal(got.view(M, times, block), want[:, None].expand(-1, times, -1))
+    del values, meta, got
+    torch.cuda.empty_cache()
