@@ -76,7 +76,8 @@ typedef enum {
   SPLR_ERR_ALIGN = 4,     /* a pointer is not 16-byte aligned                                   */
   SPLR_ERR_HIP = 5,       /* the HIP runtime reported an error while enqueueing                 */
   SPLR_ERR_WORKSPACE = 6, /* workspace NULL or smaller than splr_linear_workspace_bytes()      */
-  SPLR_ERR_SCRATCH = 7    /* splr_linear_noalloc: the call needs more than its built-in buffer  */
+  SPLR_ERR_SCRATCH = 7,   /* splr_linear_noalloc: the call needs more than its built-in buffer  */
+  SPLR_ERR_OVERLAP = 8    /* fused and grouped products: Y or the workspace overlaps an operand */
 } splr_status_t;
 
 /*
@@ -355,7 +356,8 @@ splr_status_t splr_linear_noalloc(const void* X, int64_t M, int64_t n_in, const 
  *         it makes the whole row of Y NaN, as X V^T then passes as several bfloat16 numbers, infinity
  *         minus infinity among them.
  * Errors: as splr_linear_ex; epilogue operands misaligned -> SPLR_ERR_ALIGN; activation unknown, or
- *         n_out above 2^21 -> SPLR_ERR_SHAPE.
+ *         n_out above 2^21 -> SPLR_ERR_SHAPE; Y overlapping another operand (gate and residual other
+ *         than exactly), or the needed bytes of the workspace overlapping any -> SPLR_ERR_OVERLAP.
  */
 typedef struct {
   splr_activation_t activation;

@@ -25,7 +25,7 @@ LIB_PATH = os.path.join(_PKG, "libsplr.so")
 
 SPLR_FP32, SPLR_BF16 = 0, 1
 STATUS = {0: "SPLR_OK", 1: "SPLR_ERR_NULL", 2: "SPLR_ERR_SHAPE", 3: "SPLR_ERR_DTYPE", 4: "SPLR_ERR_ALIGN",
-          5: "SPLR_ERR_HIP", 6: "SPLR_ERR_WORKSPACE", 7: "SPLR_ERR_SCRATCH"}
+          5: "SPLR_ERR_HIP", 6: "SPLR_ERR_WORKSPACE", 7: "SPLR_ERR_SCRATCH", 8: "SPLR_ERR_OVERLAP"}
 EXPORTS = ("splr_prune24_pack", "splr_prune_nm_pack", "splr_linear_ex", "splr_prune24_pack_scaled", "splr_prune24_pack_residual", "splr_packed_bytes", "splr_linear_workspace_bytes", "splr_linear",
            "splr_linear_stage1", "splr_linear_stage2", "splr_linear_stage2_dense", "splr_linear_group",
            "splr_linear_stage2_group", "splr_linear_noalloc", "splr_linear_fused", "splr_linear_experts",
@@ -615,8 +615,8 @@ def linear_fused(X: torch.Tensor, values: torch.Tensor, meta: torch.Tensor, U: O
                  stream=None) -> torch.Tensor:
     """Y [M, n_out] of y_dtype = act(X S^T + (X V^T) U^T + bias) * gate + residual, with everything
     after the products in the kernels' epilogue (splr_linear_fused). bias [n_out] of X's type; gate
-    and residual [M, n_out] of y_dtype; `out` may be gate or residual itself. The workspace holds
-    fused_workspace_bytes()."""
+    and residual [M, n_out] of y_dtype; `out` may be gate or residual itself, and overlap nothing else. The
+    workspace holds fused_workspace_bytes()."""
     return _fused_call(X, None, values, meta, U, V, bias, activation, gate, residual, y_dtype, n_out, out, workspace,
                        stream)
 

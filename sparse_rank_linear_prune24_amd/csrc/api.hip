@@ -318,12 +318,42 @@ size_t query_workspace_bytes(splr::FusedCall c) {
   return round_up(splr::fused_workspace_bytes(c), 256);
 }
 
+// Y and the workspace (`ws_bytes` of it) overlap no operand; only Y may be gate or residual itself.
+splr_status_t check_overlap(const splr::FusedCall& c, size_t ws_bytes) {
+  const size_t E = (size_t)c.experts, M = (size_t)c.M, n_in = (size_t)c.n_in, n_out = (size_t)c.n_out, r = (size_t)c.r;
+  const size_t size = c.bf16 ? 2 : 4, y_bytes = M * n_out * (c.y_bf16 ? 2 : 4);
+  const size_t TR = (n_out + 15) / 16, TK = (n_in + 63) / 64;
+  struct Range {
+    const void* p;
+    size_t bytes;
+    bool meets(const Range& o) const {
+      const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(o.p);
+      return p && o.p && bytes && o.bytes && (a < b ? b - a < bytes : a - b < o.bytes);
+    }
+  };
+  const Range y{c.Y, y_bytes}, workspace{c.workspace, ws_bytes};
+  const Range read[] = {{c.X, M * n_in * size},
+                        {c.offsets, (E + 1) * sizeof(int32_t)},
+                        {c.values, E * TR * TK * 512 * size},
+                        {c.meta, E * TR * (size_t)splr::meta_blocks((int)TK) * 1024},
+                        {r ? c.U : nullptr, E * n_out * r * size},
+                        {r ? c.V : nullptr, E * r * n_in * size},
+                        {c.ep.bias, E * n_out * size}};
+  for (const Range& x : read)
+    if (y.meets(x) || workspace.meets(x)) return SPLR_ERR_OVERLAP;
+  for (const Range& x : {Range{c.ep.gate, y_bytes}, Range{c.ep.residual, y_bytes}})
+    if (workspace.meets(x) || (x.p != c.Y && y.meets(x))) return SPLR_ERR_OVERLAP;
+  return workspace.meets(y) ? SPLR_ERR_OVERLAP : SPLR_OK;
+}
+
 // The last checks of a call with rows, then its launches.
 splr_status_t run_fused(splr::FusedCall c, size_t ws_bytes, hipStream_t stream) {
   if (!splr::prepare_fused(c)) return SPLR_ERR_SHAPE;
   const size_t need = round_up(splr::fused_workspace_bytes(c), 256);
   if (need > 0 && (!c.workspace || ws_bytes < need)) return SPLR_ERR_WORKSPACE;
   if (need > 0 && !aligned16(c.workspace)) return SPLR_ERR_ALIGN;
+  const splr_status_t s = check_overlap(c, need);
+  if (s != SPLR_OK) return s;
   return from_hip(splr::launch_fused(c, stream));
 }
 
@@ -498,6 +528,7 @@ const char* splr_status_string(splr_status_t status) {
     case SPLR_ERR_WORKSPACE: return "SPLR_ERR_WORKSPACE: workspace missing or too small";
     case SPLR_ERR_SCRATCH:
       return "SPLR_ERR_SCRATCH: the call needs more workspace than splr_linear_noalloc's built-in buffer holds";
+    case SPLR_ERR_OVERLAP: return "SPLR_ERR_OVERLAP: Y or the workspace overlaps another operand";
   }
   return "SPLR_ERR_UNKNOWN";
 }

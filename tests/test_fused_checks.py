@@ -9,7 +9,7 @@ import torch
 
 from sparse_rank_linear_prune24_amd import binding
 
-OK, NULL, SHAPE, DTYPE, ALIGN, HIP, WORKSPACE, SCRATCH = range(8)
+OK, NULL, SHAPE, DTYPE, ALIGN, HIP, WORKSPACE, SCRATCH, OVERLAP = range(9)
 A, MIS = 0x10000, 0x10008   # never dereferenced
 BIG = 1 << 40
 bf, f32 = torch.bfloat16, torch.float32
@@ -71,6 +71,41 @@ def test_workspace_sizes():
         for M, K, r in ((64, 64, 16), (1, 4096, 64), (500, 14336, 128), (8192, 4096, 64)):
             need = f(M, 32, K, r, dt)
             assert need >= M * r * 4 and fused(M=M, K=K, r=r, dt=dt, wsb=need - 1) == WORKSPACE
+
+
+@pytest.mark.skipif(os.path.exists("/dev/kfd"), reason="a call that got through would launch on made-up addresses")
+@pytest.mark.parametrize("yd", [0, 1])
+@pytest.mark.parametrize("dt", [0, 1])
+@pytest.mark.parametrize("grouped", [False, True])
+def test_overlaps_are_refused(grouped, dt, yd):
+    """Y and the workspace one entry or unit into the end of every operand, and every operand into theirs."""
+    M, K, N, r, E, size, ysize = 50, 96, 40, 16, 3 if grouped else 1, (4, 2)[dt], (4, 2)[yd]
+    L = binding.lib()
+    need = (L.splr_linear_experts_workspace_bytes(M, E, N, K, r, dt) if grouped else
+            L.splr_linear_fused_workspace_bytes(M, N, K, r, dt))
+    TR, TK = binding.tiles(N, K)
+    sizes = dict(X=M * K * size, off=4 * (E + 1), v=E * TR * TK * 512 * size, m=E * TR * 1024, U=E * N * r * size,
+                 V=E * r * K * size, bias=E * N * size, gate=M * N * ysize, residual=M * N * ysize, Y=M * N * ysize, ws=need)
+    place = {k: (i + 1) << 20 for i, k in enumerate(sizes)}
+
+    def status(**moved):
+        d = dict(place, **moved)
+        e = ep(1, d.pop("bias"), d.pop("gate"), d.pop("residual"))
+        if not grouped:
+            d.pop("off")
+        return (experts if grouped else fused)(M=M, K=K, N=N, r=r, dt=dt, yd=yd, e=e, wsb=need, **d,
+                                               **(dict(E=E) if grouped else {}))
+    for out in ("Y", "ws"):
+        for other in sizes:
+            if other == out or (other == "off" and not grouped):
+                continue
+            last = (sizes[other] - 1) // 16 * 16
+            assert status(**{out: place[other] + last}) == OVERLAP, (out, other)
+            last = (sizes[out] - 1) // 16 * 16
+            assert status(**{other: place[out] + last}) == OVERLAP, (out, other)
+            if not (out == "Y" and other in ("gate", "residual")):
+                assert status(**{out: place[other]}) == OVERLAP, (out, other)
+    assert status(Y=place["gate"], ws=place["gate"]) == OVERLAP
 
 
 # experts, n_in, n_out, rows: inside every documented limit, with more tiles than a launch of the tile kernels takes
@@ -167,3 +202,24 @@ def test_n_out_is_asked_for_when_no_shape_tells_it(host_as_device, E):
         call(E, **flat)
     with pytest.raises(binding.SplrError, match="SPLR_ERR_HIP"):
         call(E, **dict(flat, n_out=48))
+
+
+@host
+@pytest.mark.parametrize("E", [None, 3])
+def test_out_over_other_operands(host_as_device, E):
+    d = layer(E)
+    for name in ("gate", "residual"):
+        with pytest.raises(binding.SplrError, match="SPLR_ERR_HIP"):   # in place: it reaches its launch
+            call(E, **dict(d, out=d[name]))
+    both = torch.zeros(33, 48)
+    for bad in (dict(gate=both[:32], out=both[1:]), dict(residual=both[1:], out=both[:32]),
+                dict(workspace=d["out"].view(-1).view(torch.uint8)),
+                dict(y_dtype=bf, gate=None, residual=None, out=d["X"].view(-1)[:32 * 48].view(32, 48))):
+        with pytest.raises(binding.SplrError, match="SPLR_ERR_OVERLAP"):
+            call(E, **dict(d, **bad))
+    # buffers that touch without overlapping
+    halves = torch.zeros(64, 48)
+    with pytest.raises(binding.SplrError, match="SPLR_ERR_HIP"):
+        call(E, **dict(d, gate=halves[:32], out=halves[32:]))
+    with pytest.raises(binding.SplrError, match="SPLR_ERR_HIP"):
+        call(E, **dict(d, gate=halves[32:], out=halves[:32]))
