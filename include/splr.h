@@ -413,6 +413,16 @@ splr_status_t splr_linear_experts(const void* X, int64_t M, int64_t n_in, const 
                                   size_t workspace_bytes, hipStream_t stream);
 
 /*
+ * splr_linear_fused_tile -- which kernel a call of these sizes takes, as its workgroup tile: `rows`
+ * of S x `tokens` of X.  n_experts 0: splr_linear_fused, else splr_linear_experts.  16 or 32 rows x
+ * 16 or 32 tokens: the few-token kernels; 128 x 64: the tile kernel; 256 or 512 x 128 (SPLR_BF16
+ * only): the prefill kernel.  For tests and timing; the choice is no part of the contract.
+ * Errors: pointers NULL -> SPLR_ERR_NULL; sizes or types that the call refuses -> SPLR_ERR_SHAPE.
+ */
+splr_status_t splr_linear_fused_tile(int64_t M, int64_t n_experts, int64_t n_out, int64_t n_in,
+                                     int64_t r, splr_dtype_t dtype, int32_t* rows, int32_t* tokens);
+
+/*
  * splr_dense_reconstruct -- W_hat = S + U V as a dense float32 matrix (LoSparse §3: the weight is
  * approximated by the sum of the sparse and the low-rank part).  A verification aid.
  *

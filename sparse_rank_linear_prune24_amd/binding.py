@@ -29,7 +29,7 @@ STATUS = {0: "SPLR_OK", 1: "SPLR_ERR_NULL", 2: "SPLR_ERR_SHAPE", 3: "SPLR_ERR_DT
 EXPORTS = ("splr_prune24_pack", "splr_prune_nm_pack", "splr_linear_ex", "splr_prune24_pack_scaled", "splr_prune24_pack_residual", "splr_packed_bytes", "splr_linear_workspace_bytes", "splr_linear",
            "splr_linear_stage1", "splr_linear_stage2", "splr_linear_stage2_dense", "splr_linear_group",
            "splr_linear_stage2_group", "splr_linear_noalloc", "splr_linear_fused", "splr_linear_experts",
-           "splr_linear_fused_workspace_bytes", "splr_linear_experts_workspace_bytes", "splr_dense_reconstruct",
+           "splr_linear_fused_workspace_bytes", "splr_linear_experts_workspace_bytes", "splr_linear_fused_tile", "splr_dense_reconstruct",
            "splr_gram_workspace_bytes", "splr_gram_f64", "splr_chol_rinv", "splr_status_string", "splr_version")
 
 _P, _I64, _I32, _SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t
@@ -83,6 +83,8 @@ def lib() -> ctypes.CDLL:
         L.splr_linear_fused_workspace_bytes.restype = _SZ
         L.splr_linear_experts_workspace_bytes.argtypes = [_I64, _I64, _I64, _I64, _I64, _I32]
         L.splr_linear_experts_workspace_bytes.restype = _SZ
+        L.splr_linear_fused_tile.argtypes = [_I64, _I64, _I64, _I64, _I64, _I32, _P, _P]
+        L.splr_linear_fused_tile.restype = _I32
         L.splr_linear_experts.argtypes = [_P, _I64, _I64, _P, _I64, _P, _P, _I64, _P, _P, _I64, _I32, _P, _I32, _P,
                                           _P, _SZ, _P]
         L.splr_linear_experts.restype = _I32
@@ -629,6 +631,17 @@ def fused_workspace_bytes(M: int, n_out: int, n_in: int, r: int, dtype: torch.dt
 def experts_workspace_bytes(M: int, n_experts: int, n_out: int, n_in: int, r: int, dtype: torch.dtype) -> int:
     code = SPLR_BF16 if dtype == torch.bfloat16 else SPLR_FP32
     return int(lib().splr_linear_experts_workspace_bytes(M, n_experts, n_out, n_in, r, code))
+
+
+def fused_tile(M: int, n_out: int, n_in: int, r: int, dtype: torch.dtype,
+               n_experts: Optional[int] = None) -> Tuple[int, int]:
+    """The workgroup tile (rows of S, tokens) of the kernel that linear_fused, or linear_experts with
+    n_experts experts, takes for these sizes (splr_linear_fused_tile)."""
+    code = SPLR_BF16 if dtype == torch.bfloat16 else SPLR_FP32
+    rows, tokens = ctypes.c_int32(), ctypes.c_int32()
+    _check("splr_linear_fused_tile", lib().splr_linear_fused_tile(M, n_experts or 0, n_out, n_in, r, code,
+                                                                  ctypes.byref(rows), ctypes.byref(tokens)))
+    return rows.value, tokens.value
 
 
 def linear_experts(X: torch.Tensor, offsets: torch.Tensor, values: torch.Tensor, meta: torch.Tensor,

@@ -312,10 +312,23 @@ splr::FusedCall fused_call(const void* X, int64_t M, int64_t n_in, const int32_t
                          y_dtype == SPLR_BF16, workspace};
 }
 
-// Workspace of a call by its sizes (0 when it has no rows or does not fit the dispatch limits).
-size_t query_workspace_bytes(splr::FusedCall c) {
-  if (c.M == 0 || !splr::prepare_fused(c)) return 0;
-  return round_up(splr::fused_workspace_bytes(c), 256);
+// A call by its sizes, prepared, for the queries; false when it would be refused or has no rows. n_experts 0:
+// splr_linear_fused.
+bool query_call(int64_t M, int64_t n_experts, int64_t n_out, int64_t n_in, int64_t r, splr_dtype_t dtype,
+                splr::FusedCall* c) {
+  if (M < 1 || M > kMaxRows || n_out < 1 || n_out > splr::kMaxFusedOut || n_experts < 0 ||
+      n_experts > SPLR_EXPERTS_MAX || check_in(n_in) != SPLR_OK || check_rank(r) != SPLR_OK || !dtype_ok(dtype))
+    return false;
+  const int32_t any = 0;  // a non-null `offsets`: a call by expert
+  *c = fused_call(nullptr, M, n_in, n_experts ? &any : nullptr, n_experts ? n_experts : 1, nullptr, nullptr, n_out,
+                  nullptr, nullptr, r, dtype, splr::Epilogue{}, nullptr, SPLR_FP32, nullptr);
+  return splr::prepare_fused(*c);
+}
+
+size_t query_workspace_bytes(int64_t M, int64_t n_experts, int64_t n_out, int64_t n_in, int64_t r,
+                             splr_dtype_t dtype) {
+  splr::FusedCall c;
+  return query_call(M, n_experts, n_out, n_in, r, dtype, &c) ? round_up(splr::fused_workspace_bytes(c), 256) : 0;
 }
 
 // Y and the workspace (`ws_bytes` of it) overlap no operand; only Y may be gate or residual itself.
@@ -362,11 +375,18 @@ splr_status_t run_fused(splr::FusedCall c, size_t ws_bytes, hipStream_t stream) 
 extern "C" {
 
 size_t splr_linear_fused_workspace_bytes(int64_t M, int64_t n_out, int64_t n_in, int64_t r, splr_dtype_t dtype) {
-  if (M < 1 || M > kMaxRows || n_out < 1 || n_out > splr::kMaxFusedOut || check_in(n_in) != SPLR_OK ||
-      check_rank(r) != SPLR_OK || !dtype_ok(dtype))
-    return 0;
-  return query_workspace_bytes(fused_call(nullptr, M, n_in, nullptr, 1, nullptr, nullptr, n_out, nullptr, nullptr, r,
-                                          dtype, splr::Epilogue{}, nullptr, SPLR_FP32, nullptr));
+  return query_workspace_bytes(M, 0, n_out, n_in, r, dtype);
+}
+
+splr_status_t splr_linear_fused_tile(int64_t M, int64_t n_experts, int64_t n_out, int64_t n_in, int64_t r,
+                                     splr_dtype_t dtype, int32_t* rows, int32_t* tokens) {
+  if (!rows || !tokens) return SPLR_ERR_NULL;
+  splr::FusedCall c;
+  if (!query_call(M, n_experts, n_out, n_in, r, dtype, &c)) return SPLR_ERR_SHAPE;
+  const splr::FusedTile t = splr::fused_tile(c);
+  *rows = t.rows;
+  *tokens = t.tokens;
+  return SPLR_OK;
 }
 
 splr_status_t splr_linear_fused(const void* X, int64_t M, int64_t n_in, const void* values, const uint32_t* meta,
@@ -386,12 +406,7 @@ splr_status_t splr_linear_fused(const void* X, int64_t M, int64_t n_in, const vo
 
 size_t splr_linear_experts_workspace_bytes(int64_t M, int64_t n_experts, int64_t n_out, int64_t n_in, int64_t r,
                                            splr_dtype_t dtype) {
-  if (M < 0 || M > kMaxRows || n_out < 1 || n_out > splr::kMaxFusedOut || n_experts < 1 ||
-      n_experts > SPLR_EXPERTS_MAX || check_in(n_in) != SPLR_OK || check_rank(r) != SPLR_OK || !dtype_ok(dtype))
-    return 0;
-  const int32_t any = 0;  // a non-null `offsets`: a call by expert
-  return query_workspace_bytes(fused_call(nullptr, M, n_in, &any, n_experts, nullptr, nullptr, n_out, nullptr,
-                                            nullptr, r, dtype, splr::Epilogue{}, nullptr, SPLR_FP32, nullptr));
+  return n_experts < 1 ? 0 : query_workspace_bytes(M, n_experts, n_out, n_in, r, dtype);
 }
 
 splr_status_t splr_linear_experts(const void* X, int64_t M, int64_t n_in, const int32_t* offsets, int64_t n_experts,

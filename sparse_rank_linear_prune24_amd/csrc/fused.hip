@@ -68,6 +68,13 @@ bool prepare_fused(FusedCall& c) {
 
 size_t fused_workspace_bytes(const FusedCall& c) { return (size_t)c.slices * c.M * c.r * sizeof(float); }
 
+FusedTile fused_tile(const FusedCall& c) {
+  if (c.path == FusedPath::kPrefill) return {fused_prefill_rows(c), 128};
+  if (c.path == FusedPath::kTile) return {128, 64};
+  const int tokens = c.path == FusedPath::kTokens16 ? 16 : 32;
+  return {few_token_pairs(c, tokens) ? 32 : 16, tokens};
+}
+
 hipError_t launch_fused(const FusedCall& c, hipStream_t stream) {
   if (c.r > 0) {
     const hipError_t e = c.bf16 ? launch_fused_lowrank(c, stream) : launch_f32_lowrank(c, stream);

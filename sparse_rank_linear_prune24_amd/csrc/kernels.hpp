@@ -106,6 +106,11 @@ struct FusedCall {
 // its launches would exceed the dispatch limits.
 bool prepare_fused(FusedCall& c);
 size_t fused_workspace_bytes(const FusedCall& c);
+// The workgroup tile of a prepared call's second stage.
+struct FusedTile {
+  int rows, tokens;
+};
+FusedTile fused_tile(const FusedCall& c);
 hipError_t launch_fused(const FusedCall& c, hipStream_t stream);
 // Its parts. Stage 1 (T = X V^T in K slices), in bfloat16 and in float32. Stage 2: few tokens (16 or 32 a workgroup), tiles of 128 rows x 64
 // tokens, and bfloat16 tiles of 256 or 512 rows x 128 tokens.
@@ -121,6 +126,7 @@ hipError_t launch_fused_decode_f32(const FusedCall& c, int tokens, hipStream_t s
 bool fused_tile_grid_fits(const FusedCall& c);
 hipError_t launch_fused_tile(const FusedCall& c, hipStream_t stream);
 bool fused_prefill_grid_fits(const FusedCall& c);
+int fused_prefill_rows(const FusedCall& c);  // of a tile: 256 or 512
 hipError_t launch_fused_prefill(const FusedCall& c, hipStream_t stream);
 
 hipError_t launch_dense_reconstruct(const void* values, const uint32_t* meta, const void* U, const void* V,

@@ -951,6 +951,8 @@ bool fused_prefill_grid_fits(const FusedCall& c) {
   return tiles < (int64_t(1) << 22) && grid_fits(fused_tiles(c).grid, 512);
 }
 
+int fused_prefill_rows(const FusedCall& c) { return fused_tiles(c).bn; }
+
 hipError_t launch_fused_prefill(const FusedCall& c, hipStream_t stream) {
   const FusedTiles t = fused_tiles(c);
   const float* T = (const float*)c.workspace;

@@ -7,9 +7,9 @@ import pytest
 import torch
 
 from sparse_rank_linear_prune24_amd import binding
+from tests._paths import BF16, F32, SIZES
 
 pytestmark = pytest.mark.gpu
-F32, BF16 = torch.float32, torch.bfloat16
 INF, NAN = float("inf"), float("nan")
 LARGE = 3.4e38   # finite in float32, infinite in bfloat16
 
@@ -66,6 +66,7 @@ def check(got, want, bound, tag):
 SINGLE = [(1, 96, 40), (5, 64, 40), (16, 4128, 50), (12, 2112, 130), (16, 96, 8200), (9, 160, 8195), (40, 1056, 1003), (64, 544, 70),
           (20, 2080, 8195), (32, 2112, 8200), (256, 4096, 4096), (250, 4128, 4090), (2000, 1056, 4096),
           (2000, 1024, 4096), (4000, 1056, 4096), (4000, 960, 4098)]
+SINGLE += [s[3:6] for s in SIZES if s[1] is None and s[3:6] not in SINGLE]   # every kernel's
 TYPES = [BF16, F32]
 
 
@@ -87,6 +88,7 @@ def test_one_layer(M, n_in, n_out, dtype):
 # rows of 4 experts together, n_in, n_out
 GROUPED = [(8, 96, 40), (30, 2080, 1000), (64, 96, 4100), (300, 2080, 1032), (700, 1056, 1003), (4000, 1056, 2048),
            (26000, 544, 1024)]
+GROUPED += [s[3:6] for s in SIZES if s[1] and s[3:6] not in GROUPED]
 
 
 @pytest.mark.parametrize("dtype", TYPES)
