@@ -17,7 +17,8 @@
 // after it): dense U is the sum of two 2:4 matrices with fixed patterns (positions 0,1 and 2,3 of
 // every group of four ranks), so acc += U_tile T_tile^T is two structured-sparse MFMAs per 64
 // ranks with constant index operands. T (float32) enters as a bfloat16 high part plus a bfloat16
-// correction. Y is stored once.
+// correction, which rounds it to 2^-18 of itself: a third part would take half as many of these
+// MFMAs again (5 % of all at K 4096 and 128 ranks). Y is stored once.
 //
 // One kernel template for M > 64 tokens (fewer tokens take the decode kernel in decode.hip): a
 // workgroup tile of 512 rows x 128 tokens, or 256 rows when 512-row tiles would leave CUs idle;
