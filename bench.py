@@ -59,10 +59,11 @@ MALL_DEFEAT_BYTES = 640 << 20  # > 2 x (256 MB Infinity Cache + 8 x 4 MB L2)
 COUNTERS_FILE = os.path.join(ROOT, "profiles", "hbm_traffic.txt")
 REPEAT_SMALL = 8              # back-to-back launches per timed group when a step is small
 
-# kernel -> the source files it is built from (the traffic figures are tied to their hash)
+# kernel -> the source files it is built from: the kernel's own and every header they include, but for
+# kernels.hpp (declarations of host functions). The traffic figures are tied to their hash.
 KERNEL_SOURCE = {"pack": ("pack.hip", "common.hpp"),
-                 "stage2": ("linear_bf16.hip", "tile_common.hpp", "common.hpp"),
-                 "decode": ("decode.hip", "tile_common.hpp", "common.hpp")}
+                 "stage2": ("linear_bf16.hip", "tile_common.hpp", "common.hpp", "epilogue.hpp", "groups.hpp"),
+                 "decode": ("decode.hip", "tile_common.hpp", "common.hpp", "epilogue.hpp", "groups.hpp")}
 
 
 def parse():
