@@ -9,7 +9,8 @@ import torch
 
 from sparse_rank_linear_prune24_amd import binding
 
-OK, NULL, SHAPE, DTYPE, ALIGN, HIP, WORKSPACE, SCRATCH, OVERLAP = range(9)
+OK, NULL, SHAPE, DTYPE, ALIGN, HIP, WORKSPACE, SCRATCH = range(8)
+OVERLAP = 8
 A, MIS = 0x10000, 0x10008   # never dereferenced
 BIG = 1 << 40
 bf, f32 = torch.bfloat16, torch.float32
