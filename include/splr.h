@@ -352,7 +352,7 @@ splr_status_t splr_linear_noalloc(const void* X, int64_t M, int64_t n_in, const 
  *         a float32 sum.
  *         The sparse sums run over the entries that S keeps: an infinite or NaN entry of X reaches the
  *         outputs whose row of S keeps its column and no others.  (SPLR_FP32 forms sums that come out
- *         NaN a second time, one by one: with infinities a call takes up to some ms.)  With r > 0 and SPLR_BF16
+ *         NaN a second time, one by one: calls with infinities take longer.)  With r > 0 and SPLR_BF16
  *         it makes the whole row of Y NaN, as X V^T passes as several bfloat16 numbers, infinity minus
  *         infinity among them: two as in splr_linear (which rounds it to 2^-18 of itself), three in the
  *         128 x 64 tiles of splr_linear_fused_tile (exact).  With a float32 Y the number of rows thus
