@@ -57,7 +57,8 @@
 extern "C" {
 #endif
 
-typedef enum { SPLR_FP32 = 0, SPLR_BF16 = 1 } splr_dtype_t;
+/* SPLR_E4M3: 8-bit entries, only where an entry point says so. */
+typedef enum { SPLR_FP32 = 0, SPLR_BF16 = 1, SPLR_E4M3 = 2 } splr_dtype_t;
 
 /* Activations of splr_epilogue_t, evaluated in float32. */
 typedef enum {
@@ -77,7 +78,8 @@ typedef enum {
   SPLR_ERR_HIP = 5,       /* the HIP runtime reported an error while enqueueing                 */
   SPLR_ERR_WORKSPACE = 6, /* workspace NULL or smaller than splr_linear_workspace_bytes()      */
   SPLR_ERR_SCRATCH = 7,   /* splr_linear_noalloc: the call needs more than its built-in buffer  */
-  SPLR_ERR_OVERLAP = 8    /* fused and grouped products: Y or the workspace overlaps an operand */
+  SPLR_ERR_OVERLAP = 8    /* an output or the workspace overlaps an operand (fused and grouped
+                             products, splr_tokens_*, 8-bit weights)                           */
 } splr_status_t;
 
 /*
@@ -423,6 +425,132 @@ splr_status_t splr_linear_experts(const void* X, int64_t M, int64_t n_in, const 
  */
 splr_status_t splr_linear_fused_tile(int64_t M, int64_t n_experts, int64_t n_out, int64_t n_in,
                                      int64_t r, splr_dtype_t dtype, int32_t* rows, int32_t* tokens);
+
+/*
+ * splr_tokens_* -- the way of tokens to their experts and back, around splr_linear_experts and
+ * splr_linear_fp8_experts (rows sorted by expert, group offsets on the device).
+ *
+ * Token t of T has `slots` slots; slot j asks for expert ids[t][j]. An id outside 0 .. n_experts - 1
+ * names no expert here (a dropped slot, an expert on another card): the slot gets position -1 and no
+ * row. The others are sorted by expert, those of one expert by t, then j:
+ *
+ *     offsets[e] = how many slots have an id below e         positions[t][j] = the slot's row, or -1
+ *
+ * splr_tokens_dispatch -- offsets and positions from ids and, with X, the sorted rows
+ *     Xs[positions[t][j]] = X[t].
+ *   ids        [T][slots] int32 or int64 (id_bytes 4 or 8)
+ *   X          [T][D] dtype, Xs [T * slots][D] dtype; both NULL: offsets and positions only (D and dtype
+ *              are not read then)
+ *   offsets    [n_experts + 1] int32; positions [T][slots] int32
+ *   workspace  splr_tokens_dispatch_workspace_bytes() bytes (0 for few slots), clobbered; its contents on
+ *              entry do not matter. Two calls that may run at the same time need one each.
+ * splr_tokens_gather -- the rows alone, with the positions of a dispatch: Xs [rows][D].
+ * splr_tokens_combine -- the rows back to their tokens, weighted and added:
+ *     Y[t] = residual[t] + sum over j of weights[t][j] Z[positions[t][j]]
+ *   Z          [rows][D] dtype; weights [T][slots] float32, NULL for ones; residual [T][D] dtype or NULL
+ *   Y          [T][D] dtype; it may be residual itself. Without weights and residual this is the gradient
+ *              of dispatch and gather with respect to X.
+ * splr_tokens_combine_backward -- the gradient of combine for dY [T][D] dtype:
+ *     dZ[positions[t][j]] = weights[t][j] dY[t]        dweights[t][j] = sum over columns of dY[t] Z[positions[t][j]]
+ *   dZ         [rows][D] dtype or NULL; it may be Z itself. dweights [T][slots] float32 or NULL (then Z is
+ *              not read), 0 for slots without a row. (residual's gradient is dY.)
+ *
+ * Rows that no position names, those behind the last expert's among them, are left as they were. A
+ * position outside 0 .. rows - 1 counts as -1. Two slots with one position (no dispatch gives them) leave
+ * that row of Xs or dZ unspecified. T may be 0 (row buffers may be NULL then; offsets become 0), and rows too.
+ * Types: rows of SPLR_FP32 or SPLR_BF16; dispatch and gather, which copy, also of SPLR_E4M3. D is any.
+ * Arithmetic: float32 sums in the order of the slots (dweights: a fixed order of the columns), rounded
+ *         once. Weights multiply in float32, so a row of infinity or NaN reaches its own token only.
+ *         Bitwise reproducible run to run.
+ * Errors: NULL pointer -> SPLR_ERR_NULL; slots outside 1 .. SPLR_SLOTS_MAX, T not below 2^24, T * slots
+ *         or rows above 2^28, D outside 1 .. 2^20, rows of 2^36 entries or more, n_experts outside
+ *         1 .. SPLR_EXPERTS_MAX -> SPLR_ERR_SHAPE; id_bytes or dtype -> SPLR_ERR_DTYPE; rows not 16-byte
+ *         aligned, the rest not to its entries -> SPLR_ERR_ALIGN; workspace too small ->
+ *         SPLR_ERR_WORKSPACE; an output that overlaps an operand or another output (but as said) ->
+ *         SPLR_ERR_OVERLAP.
+ */
+#define SPLR_SLOTS_MAX 64
+size_t splr_tokens_dispatch_workspace_bytes(int64_t T, int64_t slots, int64_t n_experts);
+splr_status_t splr_tokens_dispatch(const void* ids, int32_t id_bytes, int64_t T, int64_t slots,
+                                   int64_t n_experts, const void* X, int64_t D, splr_dtype_t dtype,
+                                   int32_t* offsets, int32_t* positions, void* Xs, void* workspace,
+                                   size_t workspace_bytes, hipStream_t stream);
+splr_status_t splr_tokens_gather(const void* X, int64_t T, int64_t D, splr_dtype_t dtype,
+                                 const int32_t* positions, int64_t slots, void* Xs, int64_t rows,
+                                 hipStream_t stream);
+splr_status_t splr_tokens_combine(const void* Z, int64_t rows, int64_t D, splr_dtype_t dtype,
+                                  const int32_t* positions, int64_t T, int64_t slots, const float* weights,
+                                  const void* residual, void* Y, hipStream_t stream);
+splr_status_t splr_tokens_combine_backward(const void* dY, const void* Z, int64_t rows, int64_t D,
+                                           splr_dtype_t dtype, const int32_t* positions, int64_t T,
+                                           int64_t slots, const float* weights, void* dZ, float* dweights,
+                                           hipStream_t stream);
+
+/*
+ * Products with dense weights in 8 bits, for the layers that a compression leaves dense: entries in e4m3
+ * (4 exponent bits, 3 mantissa bits, largest 448, no infinities) with a float32 scale for each block, an
+ * entry standing for its value times its block's scale.
+ *
+ * splr_fp8_quantize -- X [rows][cols] (SPLR_FP32 or SPLR_BF16) to e4m3, in blocks of block_rows x 128:
+ *     s = max(largest finite magnitude in the block / 448, 2^-126)        Q = e4m3(X * (1 / s))
+ * with every step rounded to nearest even in float32. Entries that are not finite become NaN
+ * (of either sign).
+ *   block_rows 1: for activations; 128: for weights, in blocks of 128 x 128. Blocks at the edges are smaller.
+ *   transposed 0: Q [rows][cols], cols a multiple of 32; scales [ceil(cols/128)][rows] (block_rows 1: the
+ *              scales of all rows for one block of columns lie next to each other, as the products read
+ *              them) or [ceil(rows/128)][ceil(cols/128)] (128).
+ *   transposed 1: the quantisation of X^T, with blocks along X's rows: Q [cols][rows32], rows32 = rows
+ *              rounded up to a multiple of 32, zeros past the rows; scales [ceil(rows/128)][cols]
+ *              (block_rows 1) or [ceil(cols/128)][ceil(rows/128)] (128).
+ * Errors: NULL pointer -> SPLR_ERR_NULL; rows or cols outside 1 .. 2^24, more than 2^36 entries, Q's rows
+ *         above 2^20, or cols % 32 != 0 with transposed 0, or block_rows -> SPLR_ERR_SHAPE; dtype ->
+ *         SPLR_ERR_DTYPE; X or Q not 16-byte aligned, scales not 4 -> SPLR_ERR_ALIGN; overlapping buffers
+ *         -> SPLR_ERR_OVERLAP.
+ *
+ * splr_linear_fp8 -- the product with the epilogue of splr_linear_fused:
+ *     Z = X W^T + bias          Y = act(Z) * gate + residual
+ *   X          [M][n_in] dtype. SPLR_FP32 and SPLR_BF16: the call quantises it as splr_fp8_quantize does with
+ *              block_rows 1, and the quantised values are what it multiplies. SPLR_E4M3: quantised already,
+ *              with x_scales [ceil(n_in/128)][M] (otherwise not read).
+ *   W          [n_out][n_in] e4m3; w_scales [ceil(n_out/128)][ceil(n_in/128)] (w_block_rows 128) or
+ *              [ceil(n_in/128)][n_out] (w_block_rows 1)
+ *   epilogue   as splr_linear_fused; bias [n_out], gate and residual [M][n_out], all y_dtype
+ *   Y          [M][n_out] y_dtype. It may be the very buffer of gate or of residual; it must not overlap
+ *              anything else.
+ *   workspace  splr_linear_fp8_workspace_bytes() bytes (n_experts 0), clobbered. Two calls that may run
+ *              at the same time need one each.
+ * Its gradients are products of the same kind. With dY [M][n_out]: dX = dY W is the product of dY and W
+ * quantised with block_rows 128, transposed 1 (the same blocks); dW = dY^T X that of dY and X, both
+ * quantised with block_rows 1, transposed 1 (M becomes the reduction dimension, w_block_rows is 1);
+ * residual adds to a gradient that is there.
+ * Arithmetic: the sum over each block of 128 columns, times both scales (their product has to be a float32
+ *         number), added up in float32, block after block; everything after in float32, rounded once.
+ *         With a float32 Y the sums within a block are float32 too. With a bfloat16 Y large calls form them
+ *         on the 8-bit matrix instructions, which of every eight products keep what is within 2^-13 of the
+ *         largest: up to 2^-12 of the sum of absolute products, a tenth of bfloat16's own rounding on
+ *         ordinary data. NaN entries make their row or column of Y NaN. Bitwise reproducible run to run.
+ * splr_linear_fp8_experts -- the same for rows grouped by expert, as splr_linear_experts: W [n_experts][n_out][n_in],
+ *         w_scales and bias one expert after the other, offsets [n_experts + 1] int32 on the device, M may be 0.
+ * splr_linear_fp8_tile -- which kernel sizes take, as its workgroup tile (n_experts 0: splr_linear_fp8). For
+ *         tests and timing; the choice is no part of the contract.
+ * Errors: as splr_linear_fused and splr_linear_experts; w_block_rows other than 1 and 128 -> SPLR_ERR_SHAPE.
+ */
+splr_status_t splr_fp8_quantize(const void* X, int64_t rows, int64_t cols, splr_dtype_t dtype,
+                                int32_t block_rows, int32_t transposed, void* Q, float* scales,
+                                hipStream_t stream);
+size_t splr_linear_fp8_workspace_bytes(int64_t M, int64_t n_experts, int64_t n_out, int64_t n_in,
+                                       splr_dtype_t dtype, splr_dtype_t y_dtype);
+splr_status_t splr_linear_fp8(const void* X, const float* x_scales, int64_t M, int64_t n_in,
+                              splr_dtype_t dtype, const void* W, const float* w_scales, int32_t w_block_rows,
+                              int64_t n_out, const splr_epilogue_t* epilogue, splr_dtype_t y_dtype, void* Y,
+                              void* workspace, size_t workspace_bytes, hipStream_t stream);
+splr_status_t splr_linear_fp8_experts(const void* X, const float* x_scales, int64_t M, int64_t n_in,
+                                      splr_dtype_t dtype, const int32_t* offsets, int64_t n_experts,
+                                      const void* W, const float* w_scales, int32_t w_block_rows,
+                                      int64_t n_out, const splr_epilogue_t* epilogue, splr_dtype_t y_dtype,
+                                      void* Y, void* workspace, size_t workspace_bytes, hipStream_t stream);
+splr_status_t splr_linear_fp8_tile(int64_t M, int64_t n_experts, int64_t n_out, int64_t n_in,
+                                   splr_dtype_t dtype, splr_dtype_t y_dtype, int32_t* rows, int32_t* tokens);
 
 /*
  * splr_dense_reconstruct -- W_hat = S + U V as a dense float32 matrix (LoSparse §3: the weight is

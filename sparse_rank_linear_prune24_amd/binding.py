@@ -15,6 +15,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import math
 import os
 from typing import List, Optional, Sequence, Tuple
 
@@ -23,13 +24,16 @@ import torch
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libsplr.so")
 
-SPLR_FP32, SPLR_BF16 = 0, 1
+SPLR_FP32, SPLR_BF16, SPLR_E4M3 = 0, 1, 2
 STATUS = {0: "SPLR_OK", 1: "SPLR_ERR_NULL", 2: "SPLR_ERR_SHAPE", 3: "SPLR_ERR_DTYPE", 4: "SPLR_ERR_ALIGN",
           5: "SPLR_ERR_HIP", 6: "SPLR_ERR_WORKSPACE", 7: "SPLR_ERR_SCRATCH", 8: "SPLR_ERR_OVERLAP"}
 EXPORTS = ("splr_prune24_pack", "splr_prune_nm_pack", "splr_linear_ex", "splr_prune24_pack_scaled", "splr_prune24_pack_residual", "splr_packed_bytes", "splr_linear_workspace_bytes", "splr_linear",
            "splr_linear_stage1", "splr_linear_stage2", "splr_linear_stage2_dense", "splr_linear_group",
            "splr_linear_stage2_group", "splr_linear_noalloc", "splr_linear_fused", "splr_linear_experts",
            "splr_linear_fused_workspace_bytes", "splr_linear_experts_workspace_bytes", "splr_linear_fused_tile", "splr_dense_reconstruct",
+           "splr_tokens_dispatch", "splr_tokens_dispatch_workspace_bytes", "splr_tokens_gather", "splr_tokens_combine",
+           "splr_tokens_combine_backward", "splr_fp8_quantize", "splr_linear_fp8", "splr_linear_fp8_experts",
+           "splr_linear_fp8_workspace_bytes", "splr_linear_fp8_tile",
            "splr_gram_workspace_bytes", "splr_gram_f64", "splr_chol_rinv", "splr_status_string", "splr_version")
 
 _P, _I64, _I32, _SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t
@@ -88,6 +92,26 @@ def lib() -> ctypes.CDLL:
         L.splr_linear_experts.argtypes = [_P, _I64, _I64, _P, _I64, _P, _P, _I64, _P, _P, _I64, _I32, _P, _I32, _P,
                                           _P, _SZ, _P]
         L.splr_linear_experts.restype = _I32
+        L.splr_tokens_dispatch.argtypes = [_P, _I32, _I64, _I64, _I64, _P, _I64, _I32, _P, _P, _P, _P, _SZ, _P]
+        L.splr_tokens_dispatch.restype = _I32
+        L.splr_tokens_dispatch_workspace_bytes.argtypes = [_I64, _I64, _I64]
+        L.splr_tokens_dispatch_workspace_bytes.restype = _SZ
+        L.splr_tokens_gather.argtypes = [_P, _I64, _I64, _I32, _P, _I64, _P, _I64, _P]
+        L.splr_tokens_gather.restype = _I32
+        L.splr_tokens_combine.argtypes = [_P, _I64, _I64, _I32, _P, _I64, _I64, _P, _P, _P, _P]
+        L.splr_tokens_combine.restype = _I32
+        L.splr_tokens_combine_backward.argtypes = [_P, _P, _I64, _I64, _I32, _P, _I64, _I64, _P, _P, _P, _P]
+        L.splr_tokens_combine_backward.restype = _I32
+        L.splr_fp8_quantize.argtypes = [_P, _I64, _I64, _I32, _I32, _I32, _P, _P, _P]
+        L.splr_fp8_quantize.restype = _I32
+        L.splr_linear_fp8.argtypes = [_P, _P, _I64, _I64, _I32, _P, _P, _I32, _I64, _P, _I32, _P, _P, _SZ, _P]
+        L.splr_linear_fp8.restype = _I32
+        L.splr_linear_fp8_experts.argtypes = [_P, _P, _I64, _I64, _I32, _P, _I64, _P, _P, _I32, _I64, _P, _I32, _P, _P, _SZ, _P]
+        L.splr_linear_fp8_experts.restype = _I32
+        L.splr_linear_fp8_workspace_bytes.argtypes = [_I64, _I64, _I64, _I64, _I32, _I32]
+        L.splr_linear_fp8_workspace_bytes.restype = _SZ
+        L.splr_linear_fp8_tile.argtypes = [_I64, _I64, _I64, _I64, _I32, _I32, _P, _P]
+        L.splr_linear_fp8_tile.restype = _I32
         L.splr_dense_reconstruct.argtypes = [_P, _P, _P, _P, _I64, _I64, _I64, _I32, _P, _P]
         L.splr_dense_reconstruct.restype = _I32
         L.splr_gram_workspace_bytes.argtypes = [_I64, _I64]
@@ -661,6 +685,314 @@ def linear_experts(X: torch.Tensor, offsets: torch.Tensor, values: torch.Tensor,
         raise ValueError("offsets is required")
     return _fused_call(X, offsets, values, meta, U, V, bias, activation, gate, residual, y_dtype, n_out, out,
                        workspace, stream)
+
+
+SLOTS_MAX = 64  # SPLR_SLOTS_MAX
+E4M3 = torch.float8_e4m3fn
+_CODES = {torch.float32: SPLR_FP32, torch.bfloat16: SPLR_BF16, E4M3: SPLR_E4M3}
+
+
+def _on_device_of(t, name, stream):
+    """The device number and device of `t`, the call's leading tensor, and whether its device has to be made current."""
+    if not isinstance(t, torch.Tensor) or not _is_device(t):
+        raise ValueError(f"{name} must be a device tensor")
+    device = t.device
+    if stream is not None and getattr(stream, "device", device) != device:
+        raise ValueError(f"the stream belongs to {stream.device}, {name} to {device}")
+    index = t.get_device()
+    return index, device, index >= 0 and index != torch.cuda.current_device()
+
+
+def _fits(t, name, dtype, shape, index, device) -> int:
+    """The address of a contiguous tensor of this type, shape and device; `_expect` says what is wrong with another."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous()
+            and _is_device(t)):
+        if t is not None and not isinstance(t, torch.Tensor):
+            raise ValueError(f"{name} must be a device tensor")
+        _expect(t, name, dtype, math.prod(shape), device, shape)
+    return t.data_ptr()
+
+
+def _workspace(t, index):
+    """(address, bytes) of a caller's workspace, or of none."""
+    if t is None:
+        return None, 0
+    if not isinstance(t, torch.Tensor) or not _is_device(t) or t.get_device() != index or not t.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the device of the operands")
+    return t.data_ptr(), t.nbytes
+
+
+def _new(shape, dtype, device, stream):
+    """An output or workspace, allocated on the call's stream."""
+    with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _slots(t, name):
+    if not isinstance(t, torch.Tensor) or t.dim() != 2 or not 1 <= t.shape[1] <= SLOTS_MAX:
+        raise ValueError(f"{name} must be 2-D with 1 .. {SLOTS_MAX} columns")
+    return t.shape
+
+
+def _rows_type(t, name, types):
+    if t.dim() != 2 or not t.is_contiguous():
+        raise ValueError(f"{name} must be 2-D and contiguous, got shape {tuple(t.shape)}")
+    if t.dtype not in types:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected one of {', '.join(str(d) for d in types)}")
+    return _CODES[t.dtype]
+
+
+def tokens_dispatch(ids: torch.Tensor, n_experts: int, X: Optional[torch.Tensor] = None,
+                    offsets: Optional[torch.Tensor] = None, positions: Optional[torch.Tensor] = None,
+                    out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                    stream=None) -> Tuple[torch.Tensor, torch.Tensor, Optional[torch.Tensor]]:
+    """The slots of ids [T, slots] (int32 or int64) sorted by expert (splr_tokens_dispatch): offsets int32 [n_experts + 1] as
+    linear_experts takes them, positions int32 [T, slots] (-1 where the id is outside 0 .. n_experts - 1) and, with X [T, D],
+    the sorted rows `out` [T * slots, D], of which those behind offsets[n_experts] are left as they were."""
+    index, device, other = _on_device_of(ids, "ids", stream)
+    if other:
+        with torch.cuda.device(device):
+            return tokens_dispatch(ids, n_experts, X, offsets, positions, out, workspace, stream)
+    T, k = _slots(ids, "ids")
+    if ids.dtype is not torch.int64 and ids.dtype is not torch.int32 or not ids.is_contiguous():
+        raise ValueError(f"ids must be contiguous int32 or int64, got {ids.dtype}")
+    if not 1 <= n_experts <= EXPERTS_MAX:
+        raise ValueError(f"n_experts must be 1 .. {EXPERTS_MAX}, got {n_experts}")
+    if X is None and out is not None:
+        raise ValueError("out is given without X")
+    L = _lib or lib()
+    if offsets is None:
+        offsets = _new((n_experts + 1,), torch.int32, device, stream)
+    if positions is None:
+        positions = _new((T, k), torch.int32, device, stream)
+    o = _fits(offsets, "offsets", torch.int32, (n_experts + 1,), index, device)
+    p = _fits(positions, "positions", torch.int32, (T, k), index, device)
+    x = y = None
+    D = code = 0
+    if X is not None:
+        code = _rows_type(X, "X", _CODES)
+        D = X.shape[1]
+        x = _fits(X, "X", X.dtype, (T, D), index, device)
+        if out is None:
+            out = _new((T * k, D), X.dtype, device, stream)
+        y = _fits(out, "out", X.dtype, (T * k, D), index, device)
+    if workspace is None:
+        need = L.splr_tokens_dispatch_workspace_bytes(T, k, n_experts)
+        workspace = _new((need,), torch.uint8, device, stream) if need else None
+    ws, ws_bytes = _workspace(workspace, index)
+    status = L.splr_tokens_dispatch(ids.data_ptr(), ids.element_size(), T, k, n_experts, x, D, code, o, p, y, ws, ws_bytes,
+                                    _stream_handle(stream, index))
+    if status:
+        raise SplrError("splr_tokens_dispatch", status)
+    return offsets, positions, out
+
+
+def tokens_gather(X: torch.Tensor, positions: torch.Tensor, rows: Optional[int] = None, out: Optional[torch.Tensor] = None,
+                  stream=None) -> torch.Tensor:
+    """out[positions[t][j]] = X[t] (splr_tokens_gather): the rows of X [T, D] at the places that tokens_dispatch gave them. `out`
+    [rows, D], by default a new one of T * slots rows; rows that no position names are left as they were."""
+    index, device, other = _on_device_of(X, "X", stream)
+    if other:
+        with torch.cuda.device(device):
+            return tokens_gather(X, positions, rows, out, stream)
+    code = _rows_type(X, "X", _CODES)
+    T, D = X.shape
+    k = _slots(positions, "positions")[1]
+    p = _fits(positions, "positions", torch.int32, (T, k), index, device)
+    if rows is None:
+        rows = T * k if out is None else out.shape[0]
+    if out is None:
+        out = _new((rows, D), X.dtype, device, stream)
+    y = _fits(out, "out", X.dtype, (rows, D), index, device)
+    status = (_lib or lib()).splr_tokens_gather(X.data_ptr(), T, D, code, p, k, y, rows, _stream_handle(stream, index))
+    if status:
+        raise SplrError("splr_tokens_gather", status)
+    return out
+
+
+def tokens_combine(Z: torch.Tensor, positions: torch.Tensor, weights: Optional[torch.Tensor] = None,
+                   residual: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """out[t] = residual[t] + sum_j weights[t][j] Z[positions[t][j]] (splr_tokens_combine): Z [rows, D] float32 or bfloat16,
+    positions int32 [T, slots], weights float32 [T, slots] (None: ones), residual and out [T, D] of Z's type; `out` may be
+    residual itself. Without weights and residual it is the gradient of tokens_dispatch and tokens_gather."""
+    index, device, other = _on_device_of(Z, "Z", stream)
+    if other:
+        with torch.cuda.device(device):
+            return tokens_combine(Z, positions, weights, residual, out, stream)
+    code = _rows_type(Z, "Z", (torch.float32, torch.bfloat16))
+    rows, D = Z.shape
+    T, k = _slots(positions, "positions")
+    p = _fits(positions, "positions", torch.int32, (T, k), index, device)
+    w = None if weights is None else _fits(weights, "weights", torch.float32, (T, k), index, device)
+    r = None if residual is None else _fits(residual, "residual", Z.dtype, (T, D), index, device)
+    if out is None:
+        out = _new((T, D), Z.dtype, device, stream)
+    y = _fits(out, "out", Z.dtype, (T, D), index, device)
+    status = (_lib or lib()).splr_tokens_combine(Z.data_ptr(), rows, D, code, p, T, k, w, r, y, _stream_handle(stream, index))
+    if status:
+        raise SplrError("splr_tokens_combine", status)
+    return out
+
+
+def tokens_combine_backward(dY: torch.Tensor, Z: torch.Tensor, positions: torch.Tensor, weights: Optional[torch.Tensor] = None,
+                            out: Optional[torch.Tensor] = None, dweights: Optional[torch.Tensor] = None,
+                            stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """(dZ, dweights) of tokens_combine for dY [T, D] (splr_tokens_combine_backward): dZ[positions[t][j]] = weights[t][j] dY[t]
+    in `out` [rows, D], which may be Z itself and whose other rows are left as they were (a new one starts as zeros), and
+    dweights[t][j] = <dY[t], Z[positions[t][j]]>, float32 [T, slots]. The gradient of residual is dY."""
+    index, device, other = _on_device_of(dY, "dY", stream)
+    if other:
+        with torch.cuda.device(device):
+            return tokens_combine_backward(dY, Z, positions, weights, out, dweights, stream)
+    code = _rows_type(dY, "dY", (torch.float32, torch.bfloat16))
+    T, D = dY.shape
+    if not isinstance(Z, torch.Tensor) or Z.dim() != 2:
+        raise ValueError("Z must be 2-D")
+    rows, k = Z.shape[0], _slots(positions, "positions")[1]
+    z = _fits(Z, "Z", dY.dtype, (rows, D), index, device)
+    p = _fits(positions, "positions", torch.int32, (T, k), index, device)
+    w = None if weights is None else _fits(weights, "weights", torch.float32, (T, k), index, device)
+    if out is None:
+        with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
+            out = torch.zeros((rows, D), dtype=dY.dtype, device=device)
+    if dweights is None:
+        dweights = _new((T, k), torch.float32, device, stream)
+    dz = _fits(out, "out", dY.dtype, (rows, D), index, device)
+    dw = _fits(dweights, "dweights", torch.float32, (T, k), index, device)
+    status = (_lib or lib()).splr_tokens_combine_backward(dY.data_ptr(), z, rows, D, code, p, T, k, w, dz, dw,
+                                                          _stream_handle(stream, index))
+    if status:
+        raise SplrError("splr_tokens_combine_backward", status)
+    return out, dweights
+
+
+def fp8_quantize(X: torch.Tensor, block_rows: int = 1, transposed: bool = False, out: Optional[torch.Tensor] = None,
+                 scales: Optional[torch.Tensor] = None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """X [rows, cols] (float32 or bfloat16) in e4m3 with a float32 scale for each block of block_rows (1 or 128) x 128
+    (splr_fp8_quantize) -> (Q, scales). Q [rows, cols] with scales [ceil(cols/128), rows] for block_rows 1 and
+    [ceil(rows/128), ceil(cols/128)] for 128; transposed, of X^T: Q [cols, rows rounded up to 32] with scales
+    [ceil(rows/128), cols] or [ceil(cols/128), ceil(rows/128)]. As linear_fp8 takes them."""
+    index, device, other = _on_device_of(X, "X", stream)
+    if other:
+        with torch.cuda.device(device):
+            return fp8_quantize(X, block_rows, transposed, out, scales, stream)
+    code = _rows_type(X, "X", (torch.float32, torch.bfloat16))
+    if block_rows not in (1, 128):
+        raise ValueError(f"block_rows must be 1 or 128, got {block_rows}")
+    n, K = reversed(X.shape) if transposed else X.shape   # Q's rows and the entries that blocks run along
+    KB = (K + 127) // 128
+    shape = (n, (K + 31) // 32 * 32) if transposed else (n, K)
+    s_shape = (KB, n) if block_rows == 1 else ((n + 127) // 128, KB)
+    if out is None:
+        out = _new(shape, E4M3, device, stream)
+    if scales is None:
+        scales = _new(s_shape, torch.float32, device, stream)
+    q = _fits(out, "out", E4M3, shape, index, device)
+    s = _fits(scales, "scales", torch.float32, s_shape, index, device)
+    status = (_lib or lib()).splr_fp8_quantize(X.data_ptr(), X.shape[0], X.shape[1], code, block_rows, int(transposed), q, s,
+                                               _stream_handle(stream, index))
+    if status:
+        raise SplrError("splr_fp8_quantize", status)
+    return out, scales
+
+
+def _fp8_call(X, offsets, W, w_scales, x_scales, bias, activation, gate, residual, y_dtype, out, workspace, stream):
+    """linear_fp8 (offsets None) and linear_fp8_experts."""
+    index, device, other = _on_device_of(X, "X", stream)
+    if other:
+        with torch.cuda.device(device):
+            return _fp8_call(X, offsets, W, w_scales, x_scales, bias, activation, gate, residual, y_dtype, out, workspace, stream)
+    code = _rows_type(X, "X", _CODES)
+    M, n_in = X.shape
+    act = ACTIVATIONS.get(activation)
+    if act is None:
+        raise ValueError(f"activation must be one of {', '.join(ACTIVATIONS)}, got {activation!r}")
+    if y_dtype is not torch.bfloat16 and y_dtype is not torch.float32:
+        raise ValueError(f"y_dtype must be float32 or bfloat16, got {y_dtype}")
+    experts = offsets is not None
+    E = o = 0
+    lead = ()
+    if experts:
+        if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1 or not 2 <= offsets.numel() <= EXPERTS_MAX + 1:
+            raise ValueError(f"offsets must be a vector of 2 .. {EXPERTS_MAX + 1} entries")
+        E = offsets.numel() - 1
+        o = _fits(offsets, "offsets", torch.int32, (E + 1,), index, device)
+        lead = (E,)
+    if not isinstance(W, torch.Tensor) or W.dim() != 2 + len(lead):
+        raise ValueError("W must be [experts, n_out, n_in]" if experts else "W must be [n_out, n_in]")
+    n_out = W.shape[-2]
+    w = _fits(W, "W", E4M3, (*lead, n_out, n_in), index, device)
+    KB = (n_in + 127) // 128
+    blocks, by_row = (*lead, (n_out + 127) // 128, KB), (*lead, KB, n_out)
+    block_rows = 1 if isinstance(w_scales, torch.Tensor) and w_scales.shape == by_row != blocks else 128
+    ws_ = _fits(w_scales, "w_scales", torch.float32, by_row if block_rows == 1 else blocks, index, device)
+    xs = None
+    if X.dtype is E4M3:
+        xs = _fits(x_scales, "x_scales", torch.float32, (KB, M), index, device)
+    elif x_scales is not None:
+        raise ValueError("x_scales is for an X in e4m3")
+    rows = (M, n_out)
+    b = None if bias is None else _fits(bias, "bias", y_dtype, (*lead, n_out), index, device)
+    g = None if gate is None else _fits(gate, "gate", y_dtype, rows, index, device)
+    r = None if residual is None else _fits(residual, "residual", y_dtype, rows, index, device)
+    L = _lib or lib()
+    ycode = _CODES[y_dtype]
+    if out is None:
+        out = _new(rows, y_dtype, device, stream)
+    y = _fits(out, "out", y_dtype, rows, index, device)
+    if workspace is None:
+        need = L.splr_linear_fp8_workspace_bytes(M, E, n_out, n_in, code, ycode)
+        workspace = _new((need,), torch.uint8, device, stream) if need else None
+    ws, ws_bytes = _workspace(workspace, index)
+    epilogue = ctypes.byref(_Epilogue(act, b, g, r))
+    handle = _stream_handle(stream, index)
+    if experts:
+        status = L.splr_linear_fp8_experts(X.data_ptr(), xs, M, n_in, code, o, E, w, ws_, block_rows, n_out, epilogue, ycode, y,
+                                           ws, ws_bytes, handle)
+    else:
+        status = L.splr_linear_fp8(X.data_ptr(), xs, M, n_in, code, w, ws_, block_rows, n_out, epilogue, ycode, y, ws, ws_bytes,
+                                   handle)
+    if status:
+        raise SplrError("splr_linear_fp8_experts" if experts else "splr_linear_fp8", status)
+    return out
+
+
+def linear_fp8(X: torch.Tensor, W: torch.Tensor, w_scales: torch.Tensor, x_scales: Optional[torch.Tensor] = None,
+               bias: Optional[torch.Tensor] = None, activation: str = "none", gate: Optional[torch.Tensor] = None,
+               residual: Optional[torch.Tensor] = None, y_dtype: torch.dtype = torch.float32,
+               out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Y [M, n_out] of y_dtype = act(X W^T + bias) * gate + residual with W [n_out, n_in] in e4m3 (splr_linear_fp8). w_scales
+    [ceil(n_out/128), ceil(n_in/128)] (blocks of 128 x 128) or [ceil(n_in/128), n_out] (of 1 x 128). X [M, n_in] float32 or
+    bfloat16 is quantised by the call; in e4m3 it comes with x_scales [ceil(n_in/128), M]. bias [n_out], gate and residual
+    [M, n_out] of y_dtype; `out` may be gate or residual itself. The workspace holds linear_fp8_workspace_bytes()."""
+    return _fp8_call(X, None, W, w_scales, x_scales, bias, activation, gate, residual, y_dtype, out, workspace, stream)
+
+
+def linear_fp8_experts(X: torch.Tensor, offsets: torch.Tensor, W: torch.Tensor, w_scales: torch.Tensor,
+                       x_scales: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None, activation: str = "none",
+                       gate: Optional[torch.Tensor] = None, residual: Optional[torch.Tensor] = None,
+                       y_dtype: torch.dtype = torch.float32, out: Optional[torch.Tensor] = None,
+                       workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """linear_fp8 for rows grouped by expert (splr_linear_fp8_experts): rows offsets[e] .. offsets[e+1]-1 go through W[e] (W
+    [E, n_out, n_in], w_scales and bias with a leading E). offsets as linear_experts takes it, M may be 0, and rows outside
+    offsets[0] .. offsets[E]-1 of `out` are left as they were."""
+    if offsets is None:
+        raise ValueError("offsets is required")
+    return _fp8_call(X, offsets, W, w_scales, x_scales, bias, activation, gate, residual, y_dtype, out, workspace, stream)
+
+
+def linear_fp8_workspace_bytes(M: int, n_out: int, n_in: int, dtype: torch.dtype, y_dtype: torch.dtype,
+                               n_experts: Optional[int] = None) -> int:
+    return int(lib().splr_linear_fp8_workspace_bytes(M, n_experts or 0, n_out, n_in, _CODES[dtype], _CODES[y_dtype]))
+
+
+def linear_fp8_tile(M: int, n_out: int, n_in: int, dtype: torch.dtype, y_dtype: torch.dtype,
+                    n_experts: Optional[int] = None) -> Tuple[int, int]:
+    """The workgroup tile (rows of W, tokens) of the kernel that these sizes take (splr_linear_fp8_tile)."""
+    rows, tokens = ctypes.c_int32(), ctypes.c_int32()
+    _check("splr_linear_fp8_tile", lib().splr_linear_fp8_tile(M, n_experts or 0, n_out, n_in, _CODES[dtype], _CODES[y_dtype],
+                                                              ctypes.byref(rows), ctypes.byref(tokens)))
+    return rows.value, tokens.value
 
 
 def dense_reconstruct(values: torch.Tensor, meta: torch.Tensor, U: Optional[torch.Tensor],

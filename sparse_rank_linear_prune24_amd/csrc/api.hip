@@ -439,6 +439,263 @@ splr_status_t splr_linear_experts(const void* X, int64_t M, int64_t n_in, const 
 
 }  // extern "C"
 
+// ---------------------------------------------------------------- tokens to experts and back
+namespace {
+
+constexpr int64_t kMaxSlots = int64_t(1) << 28;  // T slots
+
+struct Span {
+  const void* p;
+  size_t bytes;
+  bool meets(const Span& o) const {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(o.p);
+    return p && o.p && bytes && o.bytes && (a < b ? b - a < bytes : a - b < o.bytes);
+  }
+};
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+splr_status_t check_slots(int64_t T, int64_t slots) {
+  return T >= 0 && T < kMaxRows && slots >= 1 && slots <= SPLR_SLOTS_MAX && T * slots <= kMaxSlots ? SPLR_OK : SPLR_ERR_SHAPE;
+}
+// T rows of D entries, and `rows` rows of them
+splr_status_t check_token_rows(int64_t T, int64_t rows, int64_t D, int size) {
+  if (rows < 0 || rows > kMaxSlots || D < 1 || D > kMaxCols || T * D > kMaxElems || rows * D > kMaxElems) return SPLR_ERR_SHAPE;
+  return splr::tokens_grids_fit(T, D, size) ? SPLR_OK : SPLR_ERR_SHAPE;
+}
+int entry_bytes(splr_dtype_t dtype) { return dtype == SPLR_FP32 ? 4 : dtype == SPLR_BF16 ? 2 : 1; }
+
+}  // namespace
+
+extern "C" {
+
+size_t splr_tokens_dispatch_workspace_bytes(int64_t T, int64_t slots, int64_t n_experts) {
+  if (check_slots(T, slots) != SPLR_OK || n_experts < 1 || n_experts > SPLR_EXPERTS_MAX) return 0;
+  return round_up(splr::tokens_sort_workspace_bytes(T * slots, n_experts), 256);
+}
+
+splr_status_t splr_tokens_dispatch(const void* ids, int32_t id_bytes, int64_t T, int64_t slots, int64_t n_experts,
+                                   const void* X, int64_t D, splr_dtype_t dtype, int32_t* offsets, int32_t* positions,
+                                   void* Xs, void* workspace, size_t ws_bytes, hipStream_t stream) {
+  if (!offsets || (T != 0 && (!ids || !positions)) || (T != 0 && !X != !Xs)) return SPLR_ERR_NULL;
+  splr_status_t s = check_slots(T, slots);
+  if (s == SPLR_OK && (n_experts < 1 || n_experts > SPLR_EXPERTS_MAX)) s = SPLR_ERR_SHAPE;
+  if (s != SPLR_OK) return s;
+  const bool copy = X && Xs;
+  if (id_bytes != 4 && id_bytes != 8) return SPLR_ERR_DTYPE;
+  if (copy && !dtype_ok(dtype) && dtype != SPLR_E4M3) return SPLR_ERR_DTYPE;
+  const int size = entry_bytes(dtype);
+  const int64_t N = T * slots;
+  if (copy && (s = check_token_rows(T, N, D, size)) != SPLR_OK) return s;
+  if ((reinterpret_cast<uintptr_t>(ids) & (id_bytes - 1)) || !aligned4(offsets) || !aligned4(positions) ||
+      (copy && (!aligned16(X) || !aligned16(Xs))))
+    return SPLR_ERR_ALIGN;
+  const size_t need = splr_tokens_dispatch_workspace_bytes(T, slots, n_experts);
+  if (need > 0 && (!workspace || ws_bytes < need)) return SPLR_ERR_WORKSPACE;
+  if (need > 0 && !aligned16(workspace)) return SPLR_ERR_ALIGN;
+  const Span out[] = {{offsets, (size_t)(n_experts + 1) * 4}, {positions, (size_t)N * 4},
+                      {copy ? Xs : nullptr, (size_t)N * D * size}, {workspace, need}};
+  const Span in[] = {{ids, (size_t)N * id_bytes}, {copy ? X : nullptr, (size_t)T * D * size}};
+  for (int i = 0; i < 4; ++i) {
+    for (const Span& x : in)
+      if (out[i].meets(x)) return SPLR_ERR_OVERLAP;
+    for (int j = 0; j < i; ++j)
+      if (out[i].meets(out[j])) return SPLR_ERR_OVERLAP;
+  }
+  const hipError_t e = splr::launch_tokens_sort(ids, id_bytes == 8, N, n_experts, offsets, positions, workspace, stream);
+  if (e != hipSuccess || !copy || T == 0) return from_hip(e);
+  return from_hip(splr::launch_tokens_gather(X, T, D, size, positions, slots, Xs, N, stream));
+}
+
+splr_status_t splr_tokens_gather(const void* X, int64_t T, int64_t D, splr_dtype_t dtype, const int32_t* positions,
+                                 int64_t slots, void* Xs, int64_t rows, hipStream_t stream) {
+  if (T != 0 && (!X || !positions || (rows != 0 && !Xs))) return SPLR_ERR_NULL;
+  splr_status_t s = check_slots(T, slots);
+  if (s != SPLR_OK) return s;
+  if (!dtype_ok(dtype) && dtype != SPLR_E4M3) return SPLR_ERR_DTYPE;
+  const int size = entry_bytes(dtype);
+  if ((s = check_token_rows(T, rows, D, size)) != SPLR_OK) return s;
+  if (!aligned16(X) || !aligned4(positions) || !aligned16(Xs)) return SPLR_ERR_ALIGN;
+  const Span out{Xs, (size_t)rows * D * size};
+  if (out.meets({X, (size_t)T * D * size}) || out.meets({positions, (size_t)(T * slots) * 4})) return SPLR_ERR_OVERLAP;
+  if (T == 0 || rows == 0) return SPLR_OK;
+  return from_hip(splr::launch_tokens_gather(X, T, D, size, positions, slots, Xs, rows, stream));
+}
+
+splr_status_t splr_tokens_combine(const void* Z, int64_t rows, int64_t D, splr_dtype_t dtype, const int32_t* positions,
+                                  int64_t T, int64_t slots, const float* weights, const void* residual, void* Y,
+                                  hipStream_t stream) {
+  if (T != 0 && ((rows != 0 && !Z) || !positions || !Y)) return SPLR_ERR_NULL;
+  splr_status_t s = check_slots(T, slots);
+  if (s != SPLR_OK) return s;
+  if (!dtype_ok(dtype)) return SPLR_ERR_DTYPE;
+  const int size = entry_bytes(dtype);
+  if ((s = check_token_rows(T, rows, D, size)) != SPLR_OK) return s;
+  if (!aligned16(Z) || !aligned4(positions) || !aligned4(weights) || !aligned16(residual) || !aligned16(Y)) return SPLR_ERR_ALIGN;
+  const size_t row = (size_t)D * size, N = (size_t)(T * slots);
+  const Span out{Y, (size_t)T * row};
+  if (out.meets({Z, (size_t)rows * row}) || out.meets({positions, N * 4}) || out.meets({weights, N * 4}) ||
+      (residual != Y && out.meets({residual, (size_t)T * row})))
+    return SPLR_ERR_OVERLAP;
+  if (T == 0) return SPLR_OK;
+  return from_hip(splr::launch_tokens_combine(Z, rows, D, dtype == SPLR_BF16, positions, T, slots, weights, residual, Y, stream));
+}
+
+splr_status_t splr_tokens_combine_backward(const void* dY, const void* Z, int64_t rows, int64_t D, splr_dtype_t dtype,
+                                           const int32_t* positions, int64_t T, int64_t slots, const float* weights, void* dZ,
+                                           float* dweights, hipStream_t stream) {
+  if (T != 0 && (!dY || !positions || (!dZ && !dweights && rows != 0) || (dweights && rows != 0 && !Z))) return SPLR_ERR_NULL;
+  splr_status_t s = check_slots(T, slots);
+  if (s != SPLR_OK) return s;
+  if (!dtype_ok(dtype)) return SPLR_ERR_DTYPE;
+  const int size = entry_bytes(dtype);
+  if ((s = check_token_rows(T, rows, D, size)) != SPLR_OK) return s;
+  if (!aligned16(dY) || !aligned16(Z) || !aligned4(positions) || !aligned4(weights) || !aligned16(dZ) || !aligned4(dweights))
+    return SPLR_ERR_ALIGN;
+  const size_t row = (size_t)D * size, N = (size_t)(T * slots);
+  const Span dz{dZ, (size_t)rows * row}, dw{dweights, N * 4}, z{dweights ? Z : nullptr, (size_t)rows * row};
+  const Span in[] = {{dY, (size_t)T * row}, {positions, N * 4}, {weights, N * 4}};
+  for (const Span& x : in)
+    if (dz.meets(x) || dw.meets(x)) return SPLR_ERR_OVERLAP;
+  if (dz.meets(dw) || dw.meets(z) || (dZ != Z && dz.meets(z))) return SPLR_ERR_OVERLAP;
+  if (T == 0 || (!dZ && !dweights)) return SPLR_OK;
+  return from_hip(splr::launch_tokens_combine_backward(dY, Z, rows, D, dtype == SPLR_BF16, positions, T, slots, weights, dZ,
+                                                       dweights, stream));
+}
+
+// ---------------------------------------------------------------- weights in 8 bits
+
+splr_status_t splr_fp8_quantize(const void* X, int64_t rows, int64_t cols, splr_dtype_t dtype, int32_t block_rows,
+                                int32_t transposed, void* Q, float* scales, hipStream_t stream) {
+  if (!X || !Q || !scales) return SPLR_ERR_NULL;
+  if (rows < 1 || cols < 1 || rows > kMaxRows || cols > kMaxRows || rows * cols > kMaxElems) return SPLR_ERR_SHAPE;
+  // Q's rows are the products' reduction dimension
+  if (transposed ? rows > kMaxCols : (cols % 32 != 0 || cols > kMaxCols)) return SPLR_ERR_SHAPE;
+  if (block_rows != 1 && block_rows != 128) return SPLR_ERR_SHAPE;
+  if (!dtype_ok(dtype)) return SPLR_ERR_DTYPE;
+  const bool block = block_rows == 128;
+  if (!splr::fp8_quantize_grids_fit(rows, cols, block, transposed != 0)) return SPLR_ERR_SHAPE;
+  if (!aligned16(X) || !aligned16(Q) || !aligned4(scales)) return SPLR_ERR_ALIGN;
+  const size_t R = (size_t)rows, C = (size_t)cols, rb = (R + 127) / 128, cb = (C + 127) / 128;
+  const Span x{X, R * C * entry_bytes(dtype)}, q{Q, transposed ? C * ((R + 31) / 32 * 32) : R * C},
+      sc{scales, 4 * (block ? rb * cb : transposed ? rb * C : R * cb)};
+  if (x.meets(q) || x.meets(sc) || q.meets(sc)) return SPLR_ERR_OVERLAP;
+  return from_hip(splr::launch_fp8_quantize(X, rows, cols, dtype == SPLR_BF16, block, transposed != 0, Q, scales, stream));
+}
+
+}  // extern "C"
+
+namespace {
+
+bool x_type_ok(splr_dtype_t dtype) { return dtype_ok(dtype) || dtype == SPLR_E4M3; }
+
+// The checks of both products; n_experts 0: one layer. c gets the call.
+splr_status_t check_fp8(const void* X, const float* x_scales, int64_t M, int64_t n_in, splr_dtype_t dtype,
+                        const int32_t* offsets, int64_t n_experts, const void* W, const float* w_scales, int32_t w_block_rows,
+                        int64_t n_out, const splr_epilogue_t* epilogue, splr_dtype_t y_dtype, void* Y, void* workspace,
+                        splr::Fp8Call* c) {
+  const bool experts = n_experts != 0, rows = M != 0 || !experts;
+  if (!W || !w_scales || (rows && (!X || !Y || (dtype == SPLR_E4M3 && !x_scales)))) return SPLR_ERR_NULL;
+  splr_status_t s = check_in(n_in);
+  if (s == SPLR_OK && (M < 0 || n_experts < 0 || n_experts > SPLR_EXPERTS_MAX)) s = SPLR_ERR_SHAPE;
+  if (s == SPLR_OK && rows) s = check_rows(M, n_in);
+  if (s == SPLR_OK) s = check_rows(n_out, n_in);
+  const int64_t E = experts ? n_experts : 1;
+  if (s == SPLR_OK && (E * n_out * n_in > kMaxElems || M * n_out > kMaxElems)) s = SPLR_ERR_SHAPE;
+  if (s == SPLR_OK && w_block_rows != 1 && w_block_rows != 128) s = SPLR_ERR_SHAPE;
+  if (s != SPLR_OK) return s;
+  if (!x_type_ok(dtype)) return SPLR_ERR_DTYPE;
+  splr::Epilogue ep;
+  s = check_epilogue(epilogue, y_dtype, y_dtype, n_out, &ep);
+  if (s != SPLR_OK) return s;
+  if (!aligned16(X) || !aligned16(W) || !aligned16(Y) || !aligned4(x_scales) || !aligned4(w_scales) || !aligned4(offsets))
+    return SPLR_ERR_ALIGN;
+  *c = splr::Fp8Call{X, (int)dtype, dtype == SPLR_E4M3 ? x_scales : nullptr, M, n_in, offsets, E, (const uint8_t*)W, w_scales,
+                     w_block_rows == 1, n_out, ep, Y, y_dtype == SPLR_BF16, workspace};
+  return SPLR_OK;
+}
+
+splr_status_t run_fp8(const splr::Fp8Call& c, size_t ws_bytes, hipStream_t stream) {
+  splr::Fp8Plan plan;
+  if (!splr::plan_fp8(c, &plan)) return SPLR_ERR_SHAPE;
+  const size_t need = round_up(splr::fp8_workspace_bytes(c, plan), 256);
+  if (need > 0 && (!c.workspace || ws_bytes < need)) return SPLR_ERR_WORKSPACE;
+  if (need > 0 && !aligned16(c.workspace)) return SPLR_ERR_ALIGN;
+  const size_t E = (size_t)c.experts, M = (size_t)c.M, n_in = (size_t)c.n_in, n_out = (size_t)c.n_out;
+  const size_t KB = (n_in + 127) / 128, y_size = c.y_bf16 ? 2 : 4;
+  const Span y{c.Y, M * n_out * y_size}, workspace{c.workspace, need};
+  const Span read[] = {{c.X, M * n_in * entry_bytes((splr_dtype_t)c.x_type)},
+                       {c.x_scales, M * KB * 4},
+                       {c.offsets, (E + 1) * 4},
+                       {c.W, E * n_out * n_in},
+                       {c.w_scales, E * KB * (c.w_rows ? n_out : (n_out + 127) / 128) * 4},
+                       {c.ep.bias, E * n_out * y_size}};
+  for (const Span& x : read)
+    if (y.meets(x) || workspace.meets(x)) return SPLR_ERR_OVERLAP;
+  for (const void* p : {c.ep.gate, c.ep.residual})
+    if (workspace.meets({p, y.bytes}) || (p != c.Y && y.meets({p, y.bytes}))) return SPLR_ERR_OVERLAP;
+  if (workspace.meets(y)) return SPLR_ERR_OVERLAP;
+  return from_hip(splr::launch_fp8(c, plan, stream));
+}
+
+// A call by its sizes and its plan, for the queries; false when it would be refused or has no rows. n_experts 0: one layer.
+bool query_fp8(int64_t M, int64_t n_experts, int64_t n_out, int64_t n_in, splr_dtype_t dtype, splr_dtype_t y_dtype,
+               splr::Fp8Call* c, splr::Fp8Plan* plan) {
+  if (M < 1 || M > kMaxRows || n_out < 1 || n_out > splr::kMaxFusedOut || n_experts < 0 || n_experts > SPLR_EXPERTS_MAX ||
+      check_in(n_in) != SPLR_OK || !x_type_ok(dtype) || !dtype_ok(y_dtype))
+    return false;
+  static const int32_t any = 0;  // a non-null `offsets`: a call by expert
+  *c = splr::Fp8Call{nullptr, (int)dtype, nullptr, M, n_in, n_experts ? &any : nullptr, n_experts ? n_experts : 1, nullptr,
+                     nullptr, false, n_out, splr::Epilogue{}, nullptr, y_dtype == SPLR_BF16, nullptr};
+  return splr::plan_fp8(*c, plan);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t splr_linear_fp8_workspace_bytes(int64_t M, int64_t n_experts, int64_t n_out, int64_t n_in, splr_dtype_t dtype,
+                                       splr_dtype_t y_dtype) {
+  splr::Fp8Call c;
+  splr::Fp8Plan plan;
+  return query_fp8(M, n_experts, n_out, n_in, dtype, y_dtype, &c, &plan) ? round_up(splr::fp8_workspace_bytes(c, plan), 256) : 0;
+}
+
+splr_status_t splr_linear_fp8_tile(int64_t M, int64_t n_experts, int64_t n_out, int64_t n_in, splr_dtype_t dtype,
+                                   splr_dtype_t y_dtype, int32_t* rows, int32_t* tokens) {
+  if (!rows || !tokens) return SPLR_ERR_NULL;
+  splr::Fp8Call c;
+  splr::Fp8Plan plan;
+  if (!query_fp8(M, n_experts, n_out, n_in, dtype, y_dtype, &c, &plan)) return SPLR_ERR_SHAPE;
+  *rows = plan.rows;
+  *tokens = plan.tokens;
+  return SPLR_OK;
+}
+
+splr_status_t splr_linear_fp8(const void* X, const float* x_scales, int64_t M, int64_t n_in, splr_dtype_t dtype, const void* W,
+                              const float* w_scales, int32_t w_block_rows, int64_t n_out, const splr_epilogue_t* epilogue,
+                              splr_dtype_t y_dtype, void* Y, void* workspace, size_t ws_bytes, hipStream_t stream) {
+  splr::Fp8Call c;
+  const splr_status_t s = check_fp8(X, x_scales, M, n_in, dtype, nullptr, 0, W, w_scales, w_block_rows, n_out, epilogue, y_dtype,
+                                    Y, workspace, &c);
+  return s != SPLR_OK ? s : run_fp8(c, ws_bytes, stream);
+}
+
+splr_status_t splr_linear_fp8_experts(const void* X, const float* x_scales, int64_t M, int64_t n_in, splr_dtype_t dtype,
+                                      const int32_t* offsets, int64_t n_experts, const void* W, const float* w_scales,
+                                      int32_t w_block_rows, int64_t n_out, const splr_epilogue_t* epilogue,
+                                      splr_dtype_t y_dtype, void* Y, void* workspace, size_t ws_bytes, hipStream_t stream) {
+  if (!offsets) return SPLR_ERR_NULL;
+  if (n_experts < 1) return SPLR_ERR_SHAPE;
+  splr::Fp8Call c;
+  const splr_status_t s = check_fp8(X, x_scales, M, n_in, dtype, offsets, n_experts, W, w_scales, w_block_rows, n_out, epilogue,
+                                    y_dtype, Y, workspace, &c);
+  if (s != SPLR_OK) return s;
+  return M == 0 ? SPLR_OK : run_fp8(c, ws_bytes, stream);
+}
+
+}  // extern "C"
+
 // ---------------------------------------------------------------- splr_linear_noalloc
 // For callers that cannot allocate: the first-stage workspace lives in a file-scope device array.
 // Each GPU the library runs on holds its own copy (from the first call on it until the process
