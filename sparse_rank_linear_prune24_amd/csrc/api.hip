@@ -6,7 +6,9 @@
 #include <mutex>
 
 #include "common.hpp"
+#include "fp8.hpp"
 #include "kernels.hpp"
+#include "tokens.hpp"
 
 namespace {
 

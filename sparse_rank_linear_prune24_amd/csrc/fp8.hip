@@ -1,6 +1,5 @@
 // Which kernels take a call of the product with 8-bit weights (splr_linear_fp8, splr_linear_fp8_experts).
 #include "fp8.hpp"
-#include "kernels.hpp"
 
 namespace splr {
 

@@ -5,6 +5,7 @@
 #include "common.hpp"
 #include "epilogue.hpp"
 #include "groups.hpp"
+#include "kernels.hpp"
 
 namespace splr {
 
@@ -27,6 +28,23 @@ struct Fp8Call {
   bool y_bf16;
   void* workspace;
 };
+
+// Chooses the kernel of a call with M >= 1 rows by its sizes and types; false when a launch would exceed the dispatch limits.
+struct Fp8Plan {
+  bool quantize;  // X is quantised to the workspace first
+  int rows, tokens;
+};
+bool plan_fp8(const Fp8Call& c, Fp8Plan* plan);
+size_t fp8_workspace_bytes(const Fp8Call& c, const Fp8Plan& plan);
+hipError_t launch_fp8(const Fp8Call& c, const Fp8Plan& plan, hipStream_t stream);
+// Its parts
+bool fp8_few_grid_fits(const Fp8Call& c);
+hipError_t launch_fp8_few(const Fp8Call& c, hipStream_t stream);
+
+// X [rows][cols] to e4m3 in blocks of 1 x 128 or 128 x 128 (`block`); the launch limits of that.
+bool fp8_quantize_grids_fit(int64_t rows, int64_t cols, bool block, bool transposed);
+hipError_t launch_fp8_quantize(const void* X, int64_t rows, int64_t cols, bool bf16, bool block, bool transposed, void* Q,
+                               float* scales, hipStream_t stream);
 
 #ifdef __HIPCC__
 namespace {

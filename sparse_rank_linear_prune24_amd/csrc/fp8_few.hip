@@ -6,7 +6,6 @@
 // cores: reading W is what bounds this kernel, not its matrix instructions. X that is not held in 8 bits yet is quantised in
 // registers, by the waves that use it: its blocks lie in one wave, and a launch of its own would cost more.
 #include "fp8.hpp"
-#include "kernels.hpp"
 
 namespace splr {
 namespace {

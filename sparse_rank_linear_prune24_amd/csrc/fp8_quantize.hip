@@ -1,7 +1,6 @@
 // Quantisation to e4m3 with a scale for each block (splr_fp8_quantize): s = max(largest finite magnitude / 448, 2^-126),
 // entries e4m3(x (1 / s)). Blocks of 1 x 128 or 128 x 128, the result in rows or transposed.
 #include "fp8.hpp"
-#include "kernels.hpp"
 
 namespace splr {
 namespace {

@@ -6,7 +6,6 @@
 #include <stdint.h>
 
 #include "epilogue.hpp"
-#include "fp8.hpp"
 
 namespace splr {
 
@@ -133,35 +132,6 @@ hipError_t launch_fused_prefill(const FusedCall& c, hipStream_t stream);
 hipError_t launch_dense_reconstruct(const void* values, const uint32_t* meta, const void* U, const void* V,
                                     int64_t n_out, int64_t n_in, int64_t r, bool bf16, float* W_hat,
                                     hipStream_t stream);
-
-// The way of tokens to their experts and back (tokens.hip): N = T slots sorted by expert (ids of 4 or 8 bytes), rows of D
-// entries of `size` bytes copied to their places, weighted and added back, and the gradient of that.
-size_t tokens_sort_workspace_bytes(int64_t N, int64_t experts);
-bool tokens_grids_fit(int64_t T, int64_t D, int size);
-hipError_t launch_tokens_sort(const void* ids, bool wide, int64_t N, int64_t experts, int32_t* offsets, int32_t* positions,
-                              void* workspace, hipStream_t stream);
-hipError_t launch_tokens_gather(const void* X, int64_t T, int64_t D, int size, const int32_t* positions, int64_t slots, void* Xs,
-                                int64_t rows, hipStream_t stream);
-hipError_t launch_tokens_combine(const void* Z, int64_t rows, int64_t D, bool bf16, const int32_t* positions, int64_t T,
-                                 int64_t slots, const float* weights, const void* residual, void* Y, hipStream_t stream);
-hipError_t launch_tokens_combine_backward(const void* dY, const void* Z, int64_t rows, int64_t D, bool bf16,
-                                          const int32_t* positions, int64_t T, int64_t slots, const float* weights, void* dZ,
-                                          float* dweights, hipStream_t stream);
-
-// Quantisation to e4m3 in blocks of 1 x 128 or 128 x 128 (`block`), and the products with weights so held (fp8.hpp).
-bool fp8_quantize_grids_fit(int64_t rows, int64_t cols, bool block, bool transposed);
-hipError_t launch_fp8_quantize(const void* X, int64_t rows, int64_t cols, bool bf16, bool block, bool transposed, void* Q,
-                               float* scales, hipStream_t stream);
-bool fp8_few_grid_fits(const Fp8Call& c);
-hipError_t launch_fp8_few(const Fp8Call& c, hipStream_t stream);
-// Chooses the kernel of a call with M >= 1 rows by its sizes and types; false when a launch would exceed the dispatch limits.
-struct Fp8Plan {
-  bool quantize;  // X is quantised to the workspace first
-  int rows, tokens;
-};
-bool plan_fp8(const Fp8Call& c, Fp8Plan* plan);
-size_t fp8_workspace_bytes(const Fp8Call& c, const Fp8Plan& plan);
-hipError_t launch_fp8(const Fp8Call& c, const Fp8Plan& plan, hipStream_t stream);
 
 // Cholesky QR building blocks of the low-rank step's subspace iteration (k <= kMaxCholK):
 // G = Y^T Y in float64 for float32 Y [n][k] (workspace: gram_workspace_bytes), and R^-1 (float32,

@@ -9,6 +9,7 @@
 #include "common.hpp"
 #include "epilogue.hpp"
 #include "kernels.hpp"
+#include "tokens.hpp"
 
 namespace splr {
 namespace {
