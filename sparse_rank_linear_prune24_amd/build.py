@@ -22,7 +22,8 @@ BUILD_DIR = os.path.join(ROOT, "_build")
 LIB_PATH = os.path.join(PKG, "libsplr.so")
 SOURCES = ["api.hip", "pack.hip", "residual.hip", "lowrank.hip", "linear_bf16.hip", "linear_f32.hip", "reconstruct.hip",
            "cholqr.hip", "decode.hip", "fused.hip", "fused_f32.hip",
-           "fused_tile.hip", "tokens.hip", "fp8.hip", "fp8_few.hip", "fp8_quantize.hip"]
+           "fused_tile.hip", "tokens.hip", "fp8.hip", "fp8_few.hip", "fp8_quantize.hip",
+           "fp8_tile.hip"]
 ARCH = "gfx950"
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 

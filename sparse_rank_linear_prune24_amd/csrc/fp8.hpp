@@ -40,6 +40,8 @@ hipError_t launch_fp8(const Fp8Call& c, const Fp8Plan& plan, hipStream_t stream)
 // Its parts
 bool fp8_few_grid_fits(const Fp8Call& c);
 hipError_t launch_fp8_few(const Fp8Call& c, hipStream_t stream);
+bool fp8_tile_grid_fits(const Fp8Call& c, int rows, int tokens);
+hipError_t launch_fp8_tile(const Fp8Call& c, int rows, hipStream_t stream);
 
 // X [rows][cols] to e4m3 in blocks of 1 x 128 or 128 x 128 (`block`); the launch limits of that.
 bool fp8_quantize_grids_fit(int64_t rows, int64_t cols, bool block, bool transposed);
