@@ -7,7 +7,8 @@
 // that the scales can be applied to it in float32: 16 multiply-adds for every 32 x 32 x 128 products.
 //
 // Rows lie 128 bytes apart in LDS without padding (a direct load writes 64 consecutive pieces of 16 bytes); piece c of row r
-// stands at place c ^ (r % 8) of its row, so that eight lanes that read one piece of eight rows meet all banks.
+// stands at place c ^ (r / 2 % 8) of its row, so that the 16 lanes that read 16 bytes each at a time (lanes 0 .. 3, 12 .. 15,
+// 20 .. 27 and 4 .. 11, 16 .. 19, 28 .. 31 of each half) meet every bank once.
 #include "fp8.hpp"
 #include "tile_common.hpp"
 
@@ -29,67 +30,74 @@ __device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t rs, uint8_t* 
     __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (__attribute__((address_space(3))) void*)lds, 4, offset, step_offset, 0, 0);
 }
 
-// All loads of this wave have arrived and its LDS reads are done, then workgroup barrier. The builtin wait is free; it
-// tells the compiler that nothing is outstanding.
+// All loads of this wave but the last `LATER` have arrived and its LDS reads are done, then workgroup barrier. The builtin wait
+// is free; it tells the compiler what is outstanding.
+template <int LATER>
 __device__ __forceinline__ void step_barrier() {
-  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-  __builtin_amdgcn_s_waitcnt(0);
+  static_assert(LATER < 16, "the wait's low bits");
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"i"(LATER) : "memory");
+  __builtin_amdgcn_s_waitcnt(0x0070 | LATER);
 }
 
-// 32 x 32 x 64 on e4m3 (the scaled form with no scales)
-__device__ __forceinline__ f32x16_t mfma_e4m3(i32x8_t a, i32x8_t b, f32x16_t c) {
-  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 0, 0, 0, 0, 0, 0);
-}
-__device__ __forceinline__ f32x16_t mfma_bf16(bf16x8_t a, bf16x8_t b, f32x16_t c) {
-  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
-}
-
-// A fragment: a lane's 64 bytes of a step (row lane % 32; pieces 2 (lane / 32), + 1, + 4, + 5), as e4m3 or widened
+// Fragments of 32 rows x 128 columns. A lane's part is of row lane % 32: pieces 2 h, 2 h + 1, 2 h + 4 and 2 h + 5
+// (h = lane / 32), the same for both operands.
+struct Raw {
+  u32x4_t v[4];
+  // where the first piece stands in the fragment's rows of 128 bytes; the others' places are that one ^ piece(i)
+  static __device__ __forceinline__ int first(int lane) {
+    const int row = lane % 32;
+    return row * kBlockK + ((2 * (lane / 32) ^ (row >> 1 & 7)) * 16);
+  }
+  static constexpr int piece(int i) { return 16 * (i & 1) + 64 * (i >> 1); }
+};
+// As multiplied: e4m3, or widened to bfloat16
 template <bool WIDE>
-struct Fragment;
-template <>
-struct Fragment<false> {
-  i32x8_t v[2];
-  __device__ __forceinline__ void set(const u32x4_t (&p)[4]) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[h][i] = (int)p[2 * h + i / 4][i % 4];
+struct Fragment : Raw {
+  __device__ __forceinline__ void take(const Raw& r) { static_cast<Raw&>(*this) = r; }
+  __device__ __forceinline__ i32x8_t part(int h) const {
+    return __builtin_bit_cast(i32x8_t, __builtin_shufflevector(v[2 * h], v[2 * h + 1], 0, 1, 2, 3, 4, 5, 6, 7));
   }
 };
 template <>
 struct Fragment<true> {
   bf16x8_t v[8];
-  __device__ __forceinline__ void set(const u32x4_t (&p)[4]) {
+  __device__ __forceinline__ void take(const Raw& r) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = widen_e4m3(u32x2_t{p[i / 2][2 * (i & 1)], p[i / 2][2 * (i & 1) + 1]});
+    for (int i = 0; i < 8; ++i) v[i] = widen_e4m3(u32x2_t{r.v[i / 2][2 * (i & 1)], r.v[i / 2][2 * (i & 1) + 1]});
   }
 };
-__device__ __forceinline__ f32x16_t multiply(const Fragment<false>& a, const Fragment<false>& b) {
-  f32x16_t p = {};
-  p = mfma_e4m3(a.v[0], b.v[0], p);
-  return mfma_e4m3(a.v[1], b.v[1], p);
-}
-__device__ __forceinline__ f32x16_t multiply(const Fragment<true>& a, const Fragment<true>& b) {
-  f32x16_t p = {};
+// The products' sums: token lane % 32, register 4 g + k: row 8 g + 4 (lane / 32) + k
+typedef f32x16_t Sum;
+__device__ __forceinline__ int first_row(int lane, int g) { return 8 * g + 4 * (lane / 32); }
+__device__ __forceinline__ Sum multiply(const Fragment<false>& a, const Fragment<false>& b) {
+  Sum p = {};
 #pragma unroll
-  for (int i = 0; i < 8; ++i) p = mfma_bf16(a.v[i], b.v[i], p);
+  for (int h = 0; h < 2; ++h) p = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a.part(h), b.part(h), p, 0, 0, 0, 0, 0, 0);
+  return p;
+}
+__device__ __forceinline__ Sum multiply(const Fragment<true>& a, const Fragment<true>& b) {
+  Sum p = {};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) p = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.v[i], b.v[i], p, 0, 0, 0);
   return p;
 }
 
-// WR x WT waves, each NR x NT fragments of 32 rows of W x 32 tokens.
+// WR x WT waves, each NR x NT fragments: a workgroup tile of 32 WR NR rows of W x 32 WT NT tokens.
 template <int WR, int WT, int NR, int NT>
 struct Shape {
-  static constexpr int kWaves = WR * WT, kThreads = kWaves * kWave, kRows = WR * NR * 32, kTokens = WT * NT * 32;
-  static constexpr int kStage = (kRows + kTokens) * (kBlockK + 4);  // bytes of a step: both operands and their scales
-  static constexpr int kPitch = NR * 32 + 4;                        // floats of a token's row in the epilogue
-  static constexpr int kLds = 2 * kStage > kWaves * 32 * kPitch * 4 ? 2 * kStage : kWaves * 32 * kPitch * 4;
+  static constexpr int kWaves = WR * WT, kThreads = kWaves * kWave, kWaveRows = NR * 32, kWaveTokens = NT * 32;
+  static constexpr int kRows = WR * kWaveRows, kTokens = WT * kWaveTokens;
+  static constexpr int kStage = (kRows + kTokens) * kBlockK;  // LDS of a step's operands: two of them, then
+  static constexpr int kScales = (kRows + kTokens) * 4;       // four steps' scales, and what nobody reads
+  static constexpr int kSpare = 2 * kStage + 4 * kScales, kAll = kSpare + kWaves * 256;
+  static constexpr int kPitch = kWaveRows + 4, kEpilogue = kWaves * 32 * kPitch * 4;  // floats of a token's row in the epilogue
+  static constexpr int kLds = kAll > kEpilogue ? kAll : kEpilogue;
 };
 
 template <int WR, int WT, int NR, int NT, bool WIDE, bool W_ROWS, bool EXPERTS>
 __global__ __launch_bounds__(WR * WT * kWave, 2) void fp8_tile_kernel(
     const uint8_t* __restrict__ X, const float* __restrict__ x_scales, const uint8_t* __restrict__ W,
-    const float* __restrict__ w_scales, Epilogue ep, void* Y, int y_bf16, int M, int K, int n_out, int tiles_n, Groups groups) {
+    const float* __restrict__ w_scales, Epilogue ep, void* Y, int past_caches, int M, int K, int n_out, int tiles_n, Groups groups) {
   using S = Shape<WR, WT, NR, NT>;
   constexpr int BN = S::kRows, BM = S::kTokens, kWaves = S::kWaves;
   __shared__ __align__(1024) uint8_t lds[S::kLds];
@@ -119,170 +127,229 @@ __global__ __launch_bounds__(WR * WT * kWave, 2) void fp8_tile_kernel(
   const int group = tile / (kGroupM * tiles_n), in_group = tile - group * kGroupM * tiles_n;
   const int group_m = min(kGroupM, tiles_m - group * kGroupM);
   const int m0 = (group * kGroupM + in_group % group_m) * BM, n0 = in_group / group_m * BN;
-  const int wave_n = wave / WT * NR * 32, wave_m = wave % WT * NT * 32;  // of the tile
+  const int wave_n = wave / WT * S::kWaveRows, wave_m = wave % WT * S::kWaveTokens;  // of the tile
 
-  // What a wave loads: pieces of eight rows, a lane 16 bytes of one; rows past the last and columns past K come as zeros
+  // What a wave loads: pieces of eight rows, a lane 16 bytes of one. Columns past K come as zeros; rows past the last are
+  // the last one again, and their results are not stored.
   const int rows_n = min(BN, n_out - n0), rows_m = min(BM, M - m0);
-  const __amdgpu_buffer_rsrc_t wrs =
-      __builtin_amdgcn_make_buffer_rsrc((void*)(W + (e * n_out + n0) * K), (short)0, rows_n * K, kBuffer);
-  const __amdgpu_buffer_rsrc_t xrs =
-      __builtin_amdgcn_make_buffer_rsrc((void*)(X + (row0 + m0) * K), (short)0, rows_m * K, kBuffer);
-  const int l_row = lane >> 3, l_col = ((lane & 7) ^ l_row) * 16;
+  const uint8_t *const w0 = W + (e * n_out + n0) * K, *const x0 = X + (row0 + m0) * K;
+  int l_row = 8 * wave + (lane >> 3);
+  const int l_col = ((lane & 7) ^ (4 * (wave & 1) + (lane >> 4))) * 16;
+  static_assert(kWaves % 2 == 0, "a wave's pieces are all even or all odd");
   constexpr int kLoadsW = BN / 8 / kWaves, kLoadsX = BM / 8 / kWaves;
   static_assert(BN % (8 * kWaves) == 0 && BM % (8 * kWaves) == 0, "whole pieces");
-  int w_off[kLoadsW], x_off[kLoadsX];
-#pragma unroll
-  for (int t = 0; t < kLoadsW; ++t) w_off[t] = (8 * (wave + kWaves * t) + l_row) * K + l_col;
-#pragma unroll
-  for (int t = 0; t < kLoadsX; ++t) x_off[t] = (8 * (wave + kWaves * t) + l_row) * K + l_col;
-  constexpr int kX = BN * kBlockK, kScaleX = (BN + BM) * kBlockK, kScaleW = kScaleX + BM * 4;  // in a stage
+  constexpr int kX = BN * kBlockK, kScaleW = BM * 4;  // in a step's operands, in its scales
   const float* const w_scale = w_scales + e * KB * (W_ROWS ? n_out : (n_out + 127) / 128);
-  auto load = [&](int kb, int stage) __attribute__((always_inline)) {
-    uint8_t* const to = lds + stage * S::kStage;
-    if (kb == KB - 1 && K % kBlockK) {  // nothing is loaded after this step
-      const int away = kb * kBlockK + l_col >= K ? kAway : 0;
-#pragma unroll
-      for (int t = 0; t < kLoadsW; ++t) w_off[t] += away;
-#pragma unroll
-      for (int t = 0; t < kLoadsX; ++t) x_off[t] += away;
-    }
-#pragma unroll
-    for (int t = 0; t < kLoadsW; ++t) load_to_lds<16>(wrs, to + (wave + kWaves * t) * 1024, w_off[t], kb * kBlockK);
-#pragma unroll
-    for (int t = 0; t < kLoadsX; ++t) load_to_lds<16>(xrs, to + kX + (wave + kWaves * t) * 1024, x_off[t], kb * kBlockK);
-    if (wave < BM / 64) {
-      const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
-          (void*)(x_scales + (size_t)kb * all_rows + row0 + m0), (short)0, rows_m * 4, kBuffer);
-      load_to_lds<4>(rs, to + kScaleX + wave * 256, (wave * 64 + lane) * 4, 0);
-    } else if (W_ROWS && wave - BM / 64 < BN / 64) {
+  // A wave's 64 scales: the tokens', then the rows' of W; one with none loads nothing to a place that nobody reads.
+  const bool of_x = wave < BM / 64, of_w = W_ROWS && !of_x && wave < BM / 64 + BN / 64;
+  const int scales_first = (of_x ? wave : wave - BM / 64) * 64, scales_end = (of_x ? rows_m : rows_n) * 4;
+  const float* const scales0 = of_x ? x_scales + row0 + m0 : w_scale + n0;
+  const int64_t scales_step = of_x ? all_rows : n_out;
+  const int scales_ring = of_x || of_w ? 3 : 0;
+  const int scales_to = of_x   ? 2 * S::kStage + scales_first * 4
+                        : of_w ? 2 * S::kStage + kScaleW + scales_first * 4
+                               : S::kSpare + wave * 256;
+  const int scales_off = of_x || of_w ? (scales_first + lane) * 4 : kAway;
+  // Load d of a step. Of a step past the last nothing is read, and zeros are written. No branches, here and in the loop:
+  // across them the compiler would move the multiply-adds away from the matrix instructions that they belong to.
+  constexpr int kLoads = kLoadsW + kLoadsX + 1;
+  auto load = [&](int kb, int d) __attribute__((always_inline)) {
+    if (d == kLoads - 1) {
       const __amdgpu_buffer_rsrc_t rs =
-          __builtin_amdgcn_make_buffer_rsrc((void*)(w_scale + (size_t)kb * n_out + n0), (short)0, rows_n * 4, kBuffer);
-      load_to_lds<4>(rs, to + kScaleW + (wave - BM / 64) * 256, ((wave - BM / 64) * 64 + lane) * 4, 0);
+          __builtin_amdgcn_make_buffer_rsrc((void*)(scales0 + kb * scales_step), (short)0, scales_end, kBuffer);
+      load_to_lds<4>(rs, lds + scales_to + (kb & scales_ring) * S::kScales, kb < KB ? scales_off : kAway, 0);
+    } else {
+      const bool of_w = d < kLoadsW;
+      const int t = kWaves * (of_w ? d : d - kLoadsW);
+      asm("" : "+v"(l_row));  // the rows' offsets are formed here each time: there are no registers to keep them in
+      const int rows = of_w ? rows_n : rows_m;
+      const __amdgpu_buffer_rsrc_t rs =
+          __builtin_amdgcn_make_buffer_rsrc((void*)(of_w ? w0 : x0), (short)0, rows * K, kBuffer);
+      load_to_lds<16>(rs, lds + (kb & 1) * S::kStage + (of_w ? 0 : kX) + (wave + t) * 1024,
+                      __umul24(min(l_row + 8 * t, rows - 1), K) + (kb * kBlockK + l_col < K ? l_col : kAway),
+                      kb * kBlockK);
     }
   };
   static_assert(!W_ROWS || BM / 64 + BN / 64 <= kWaves, "a wave for each 64 scales");
 
-  const int sub = lane & 31, half = lane >> 5;
-  // a lane's four pieces of its row: 2 half, 2 half + 1, and those + 4
-  int at[4];
+  // A lane's pieces of a fragment. Their places are formed at each read (the asm hides that they are the same), which takes
+  // fewer registers than keeping them.
+  int at = Raw::first(lane);
+  auto read = [&](const uint8_t* rows, Raw& r) __attribute__((always_inline)) {
+    asm("" : "+v"(at));
 #pragma unroll
-  for (int i = 0; i < 4; ++i) at[i] = sub * kBlockK + (((2 * half + (i & 1) + 4 * (i >> 1)) ^ (sub & 7)) * 16);
-  auto read = [&](const uint8_t* rows, u32x4_t (&p)[4]) __attribute__((always_inline)) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) p[i] = *(const u32x4_t*)(rows + at[i]);
+    for (int i = 0; i < 4; ++i) r.v[i] = *(const u32x4_t*)(rows + (at ^ Raw::piece(i)));
   };
 
-  f32x16_t acc[NR][NT];
+  // The steps. p of a fragment is added to the sums while the next one's matrix instructions run; the last one's in the next
+  // step. A step's last LDS reads lie before its last column of fragments: there the waves meet, the step's place in LDS takes
+  // the loads of the step after next, and the next one's first fragments are read as the present ones are done with.
+  using F = Fragment<WIDE>;
+  constexpr int kBlocks = NR * NT;
+  static_assert(NT % 2 == 0, "rings with constant indexes");
+  F a[NR], b[2];
+  Raw raw;  // WIDE: of the next column of fragments
+  Sum acc[NR][NT], p[2];
+  float s[2] = {0.0f, 0.0f};  // scales of this column's tokens, and the last's
 #pragma unroll
   for (int i = 0; i < NR; ++i)
 #pragma unroll
-    for (int j = 0; j < NT; ++j) acc[i][j] = f32x16_t{};
-  const float* sw_block = w_scale + (size_t)(min(n0 + wave_n, n_out - 1) / 128) * KB;
-  load(0, 0);
-  for (int kb = 0; kb < KB; ++kb) {
-    const int stage = kb & 1;
-    const float sw = W_ROWS ? 1.0f : sw_block[kb];
-    step_barrier();
-    if (kb + 1 < KB) load(kb + 1, stage ^ 1);
-    const uint8_t* const w = lds + stage * S::kStage + wave_n * kBlockK;
-    const uint8_t* const x = lds + stage * S::kStage + kX + wave_m * kBlockK;
-    const float* const sx = (const float*)(lds + stage * S::kStage + kScaleX) + wave_m + sub;
-    const float* const sr = (const float*)(lds + stage * S::kStage + kScaleW) + wave_n + 4 * half;
-    float s[NT];
-#pragma unroll
-    for (int j = 0; j < NT; ++j) s[j] = sx[32 * j] * sw;
-    Fragment<WIDE> a[NR], b[2];
-    u32x4_t raw[4];
-    read(w, raw);
-    a[0].set(raw);
-    read(x, raw);
-    b[0].set(raw);
-#pragma unroll
-    for (int i = 1; i < NR; ++i) {
-      read(w + i * 32 * kBlockK, raw);
-      a[i].set(raw);
+    for (int j = 0; j < NT; ++j) acc[i][j] = Sum{};
+  p[0] = p[1] = Sum{};
+  const float* const sw_block = w_scale + (size_t)(min(n0 + wave_n, n_out - 1) / 128) * KB;
+  const float* const x_scale = (const float*)(lds + 2 * S::kStage) + wave_m + lane % 32;
+  const float* const r_scale = (const float*)(lds + 2 * S::kStage + kScaleW) + wave_n;
+  auto read_now = [&](const uint8_t* rows, F& f) __attribute__((always_inline)) {
+    if constexpr (WIDE) {
+      Raw r;
+      read(rows, r);
+      f.take(r);
+    } else {
+      read(rows, f);
     }
-    // One group for each fragment of the result: its matrix instructions, and while they run the multiply-adds of the one
-    // before and the reads of the next column of fragments
-    f32x16_t p[2];
-    auto scale = [&](int i, int j, const f32x16_t& q) __attribute__((always_inline)) {
+  };
+  auto add = [&](int kb, auto tt) __attribute__((always_inline)) {  // p of fragment t of step kb
+    constexpr int t = decltype(tt)::value, i = t % NR, j = t / NR;
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        if constexpr (W_ROWS) {
-          const f32x4_t r = *(const f32x4_t*)(sr + 32 * i + 8 * g);
+    for (int g = 0; g < 4; ++g) {
+      f32x4_t by = {s[j & 1], s[j & 1], s[j & 1], s[j & 1]};
+      if constexpr (W_ROWS) by *= *(const f32x4_t*)(r_scale + (kb & 3) * (S::kScales / 4) + i * 32 + first_row(lane, g));
 #pragma unroll
-          for (int k = 0; k < 4; ++k) acc[i][j][4 * g + k] = fmaf(q[4 * g + k], s[j] * r[k], acc[i][j][4 * g + k]);
+      for (int k = 0; k < 4; ++k) acc[i][j][4 * g + k] = fmaf(p[t & 1][4 * g + k], by[k], acc[i][j][4 * g + k]);
+    }
+  };
+  // A step's loads are spread over kSpread fragments from its last column on, so that no wave waits with its matrix
+  // instructions behind a queue of loads.
+  constexpr int kSpread = NR + 1, kEachLoads = (kLoads + kSpread - 1) / kSpread;
+  static_for<kLoads>([&](auto d) __attribute__((always_inline)) { load(0, decltype(d)::value); });
+  constexpr int kFirst = NR * kEachLoads < kLoads ? NR * kEachLoads : kLoads;  // issued in the step itself
+  static_for<kFirst>([&](auto d) __attribute__((always_inline)) { load(1, decltype(d)::value); });
+  step_barrier<kFirst>();
+  float sw = W_ROWS ? 1.0f : sw_block[0];
+#pragma unroll
+  for (int i = 0; i < NR; ++i) read_now(lds + (wave_n + i * 32) * kBlockK, a[i]);
+  read_now(lds + kX + wave_m * kBlockK, b[0]);
+  for (int kb = 0; kb < KB; ++kb) {
+    const uint8_t* const x = lds + (kb & 1) * S::kStage + kX + wave_m * kBlockK;
+    const uint8_t* const next = lds + (~kb & 1) * S::kStage;  // after the last step: of what lies there
+    const float sw_next = W_ROWS ? 1.0f : sw_block[min(kb + 1, KB - 1)];
+    static_for<kBlocks>([&](auto tt) __attribute__((always_inline)) {
+      constexpr int t = decltype(tt)::value, i = t % NR, j = t / NR;
+      if constexpr (i == 0) {
+        if constexpr (j + 1 < NT) {
+          if constexpr (WIDE) read(x + (j + 1) * 32 * kBlockK, raw);
+          else read(x + (j + 1) * 32 * kBlockK, b[(j + 1) & 1]);
         } else {
-#pragma unroll
-          for (int k = 0; k < 4; ++k) acc[i][j][4 * g + k] = fmaf(q[4 * g + k], s[j], acc[i][j][4 * g + k]);
+          step_barrier<0>();
+          if constexpr (WIDE) read(next + kX + wave_m * kBlockK, raw);
+          else read(next + kX + wave_m * kBlockK, b[0]);
         }
       }
-    };
-    static_for<NR * NT>([&](auto tt) __attribute__((always_inline)) {
-      constexpr int t = decltype(tt)::value, i = t % NR, j = t / NR;
-      if constexpr (i == 0 && j + 1 < NT) read(x + (j + 1) * 32 * kBlockK, raw);
-      p[t & 1] = multiply(a[i], b[j & 1]);
-      if constexpr (t > 0) scale((t - 1) % NR, (t - 1) / NR, p[(t - 1) & 1]);
-      if constexpr (i == NR - 1 && j + 1 < NT) b[(j + 1) & 1].set(raw);
+      constexpr int kTurn = t >= kBlocks - NR ? t - (kBlocks - NR) : t + NR;  // of the spread loads
+      constexpr int kFrom = kTurn * kEachLoads;
+      constexpr int kCount = kFrom >= kLoads ? 0 : kLoads - kFrom < kEachLoads ? kLoads - kFrom : kEachLoads;
+      static_for<kCount>([&](auto d) __attribute__((always_inline)) {
+        load(t >= kBlocks - NR ? kb + 2 : kb + 1, kFrom + decltype(d)::value);
+      });
+      const Sum now = multiply(a[i], b[j & 1]);
+      add(t > 0 ? kb : kb - 1, std::integral_constant<int, (t + kBlocks - 1) % kBlocks>{});
+      p[t & 1] = now;
+      if constexpr (i == 0) s[j & 1] = x_scale[(kb & 3) * (S::kScales / 4) + 32 * j] * sw;
+      if constexpr (WIDE && i == NR - 1) b[(j + 1) & 1].take(raw);
       constexpr int kInstructions = WIDE ? 8 : 2, kEach = WIDE ? 4 : 8;
 #pragma unroll
       for (int k = 0; k < kInstructions; ++k) {
         __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);      // a matrix instruction
         __builtin_amdgcn_sched_group_barrier(0x002, kEach, 0);  // vector instructions
+        if (k < kCount) __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);  // a load
       }
       __builtin_amdgcn_sched_barrier(0);
+      if constexpr (j == NT - 1) read_now(next + (wave_n + i * 32) * kBlockK, a[i]);
     });
-    scale(NR - 1, NT - 1, p[(NR * NT - 1) & 1]);
+    sw = sw_next;
   }
+  add(KB - 1, std::integral_constant<int, kBlocks - 1>{});
   // The result through LDS, 32 tokens at a time in a part of each wave's own, so that loads and stores of the epilogue take
-  // whole token rows of the wave's 32 NR outputs. D fragment: token lane % 32, rows 8 g + 4 (lane / 32) .. + 3.
-  step_barrier();
-  constexpr int kLanes = NR * 8, kRound = kWave / kLanes;  // lanes a token row, tokens at a time
+  // whole token rows of the wave's outputs. All of a part's loads, then all its sums, then all its stores: no branch between.
+  step_barrier<0>();
+  constexpr int kLanes = S::kWaveRows / 4, kRound = kWave / kLanes, kRounds = 32 / kRound;
+  constexpr bool kBf16 = !WIDE;  // Y's type
   float* const mine = (float*)lds + wave * 32 * S::kPitch;
   const int c = lane % kLanes * 4, n = n0 + wave_n + c, left = n_out - n;
-  const bool vec = left >= 4 && n_out % 4 == 0;
-  const f32x4_t none = {0, 0, 0, 0};
-  const f32x4_t bias = ep.bias && left > 0 ? load4(ep.bias, e * n_out + n, ep.bias_bf16, vec, left) : none;
+  const bool vec = n_out % 4 == 0 && left >= 4;
+  const f32x4_t bias = ep.bias && left > 0 ? load4(ep.bias, e * n_out + n, kBf16, vec, left) : f32x4_t{0, 0, 0, 0};
+  // whole: every entry of the wave's exists, four aligned; past: stores that pass the caches
+  const auto finish = [&](auto whole, auto past) __attribute__((always_inline)) {
+    static_for<NT>([&](auto jj) __attribute__((always_inline)) {
+      constexpr int j = decltype(jj)::value;
+      u32x4_t gate[kRounds], residual[kRounds];
+      f32x4_t y[kRounds];
+      const auto place = [&](int r, size_t& at) __attribute__((always_inline)) {  // of a lane's four entries in round r
+        const int m = m0 + wave_m + 32 * j + r * kRound + lane / kLanes;
+        at = (row0 + m) * n_out + n;
+        return decltype(whole)::value || (m < M && left > 0);
+      };
+      const auto load = [&](const void* p, u32x4_t (&v)[kRounds]) __attribute__((always_inline)) {
 #pragma unroll
-  for (int j = 0; j < NT; ++j) {
+        for (int r = 0; r < kRounds; ++r) {
+          size_t at;
+          if (place(r, at)) v[r] = load_raw4(p, at, kBf16, decltype(whole)::value || vec, left);
+          else v[r] = u32x4_t{0, 0, 0, 0};
+        }
+      };
+      if (ep.gate) load(ep.gate, gate);
+      if (ep.residual) load(ep.residual, residual);
 #pragma unroll
-    for (int i = 0; i < NR; ++i)
+      for (int i = 0; i < NR; ++i)
 #pragma unroll
-      for (int g = 0; g < 4; ++g)
-        *(f32x4_t*)(mine + sub * S::kPitch + 32 * i + 8 * g + 4 * half) =
-            f32x4_t{acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]};
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        for (int g = 0; g < 4; ++g) {
+          const Sum& v = acc[i][j];
+          *(f32x4_t*)(mine + lane % 32 * S::kPitch + i * 32 + first_row(lane, g)) =
+              f32x4_t{v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]};
+        }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
-    for (int r = 0; r < 32; r += kRound) {
-      const int token = r + lane / kLanes, m = m0 + wave_m + 32 * j + token;
-      const f32x4_t sum = *(const f32x4_t*)(mine + token * S::kPitch + c);
-      if (m < M && left > 0) {
-        const size_t where = (row0 + m) * n_out + n;
-        const f32x4_t gate = ep.gate ? load4(ep.gate, where, y_bf16, vec, left) : none;
-        const f32x4_t residual = ep.residual ? load4(ep.residual, where, y_bf16, vec, left) : none;
-        store4<false>(Y, where, y_bf16, vec, left, finish4(sum, bias, ep, gate, residual));
+      for (int r = 0; r < kRounds; ++r) y[r] = *(const f32x4_t*)(mine + (r * kRound + lane / kLanes) * S::kPitch + c) + bias;
+      with_activation(ep.act, [&](auto act) __attribute__((always_inline)) {
+#pragma unroll
+        for (int r = 0; r < kRounds; ++r) y[r] = activate4<decltype(act)::value>(y[r]);
+      });
+      if (ep.gate) {
+#pragma unroll
+        for (int r = 0; r < kRounds; ++r) y[r] *= widen4(gate[r], kBf16);
       }
-    }
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  }
+      if (ep.residual) {
+#pragma unroll
+        for (int r = 0; r < kRounds; ++r) y[r] += widen4(residual[r], kBf16);
+      }
+#pragma unroll
+      for (int r = 0; r < kRounds; ++r) {
+        size_t at;
+        if (place(r, at)) store4<decltype(past)::value>(Y, at, kBf16, decltype(whole)::value || vec, left, y[r]);
+      }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    });
+  };
+  // A Y too large for the caches goes past them: the rows of X and W that later tiles read stay there instead.
+  if (n_out % 4 != 0 || n0 + wave_n + S::kWaveRows > n_out || m0 + wave_m + S::kWaveTokens > M) finish(std::false_type{}, std::false_type{});
+  else if (past_caches) finish(std::true_type{}, std::true_type{});
+  else finish(std::true_type{}, std::false_type{});
 }
 
 int64_t tile_blocks(const Fp8Call& c, int tokens) {
   return c.offsets ? most_group_tiles(c.M, c.experts, tokens) : ceil_div(c.M, tokens);
 }
 
-template <int WR, int WT, int NR, int NT, bool WIDE>
+template <int WR, int WT, int NR, int NT, bool WIDE, bool W_ROWS>
 hipError_t launch_shape(const Fp8Call& c, hipStream_t stream) {
   using S = Shape<WR, WT, NR, NT>;
   const int tiles_n = (int)ceil_div(c.n_out, S::kRows);
   const dim3 grid((unsigned)(8 * ceil_div(tiles_n * tile_blocks(c, S::kTokens), 8)));
   const Groups groups{c.offsets, (int)c.experts, (int)c.M};
-  const auto launch = [&](auto kernel) {
-    kernel<<<grid, dim3(S::kThreads), 0, stream>>>((const uint8_t*)c.X, c.x_scales, c.W, c.w_scales, c.ep, c.Y, c.y_bf16 ? 1 : 0,
-                                                   (int)c.M, (int)c.n_in, (int)c.n_out, tiles_n, groups);
-  };
-  if (c.w_rows) launch(c.offsets ? fp8_tile_kernel<WR, WT, NR, NT, WIDE, true, true> : fp8_tile_kernel<WR, WT, NR, NT, WIDE, true, false>);
-  else launch(c.offsets ? fp8_tile_kernel<WR, WT, NR, NT, WIDE, false, true> : fp8_tile_kernel<WR, WT, NR, NT, WIDE, false, false>);
+  const int past = (double)c.M * c.n_out * (WIDE ? 4 : 2) > kNonTemporalYBytes;
+  const auto kernel = c.offsets ? fp8_tile_kernel<WR, WT, NR, NT, WIDE, W_ROWS, true> : fp8_tile_kernel<WR, WT, NR, NT, WIDE, W_ROWS, false>;
+  kernel<<<grid, dim3(S::kThreads), 0, stream>>>((const uint8_t*)c.X, c.x_scales, c.W, c.w_scales, c.ep, c.Y,
+                                                 past, (int)c.M, (int)c.n_in, (int)c.n_out, tiles_n, groups);
   return hipGetLastError();
 }
 
@@ -293,8 +360,12 @@ bool fp8_tile_grid_fits(const Fp8Call& c, int rows, int tokens) {
 }
 
 hipError_t launch_fp8_tile(const Fp8Call& c, int rows, hipStream_t stream) {
-  if (rows == 256) return c.y_bf16 ? launch_shape<4, 2, 2, 4, false>(c, stream) : launch_shape<4, 2, 2, 2, true>(c, stream);
-  return c.y_bf16 ? launch_shape<2, 2, 2, 2, false>(c, stream) : launch_shape<2, 2, 2, 2, true>(c, stream);
+  if (rows == 256) {
+    if (!c.y_bf16) return c.w_rows ? launch_shape<4, 2, 2, 2, true, true>(c, stream) : launch_shape<4, 2, 2, 2, true, false>(c, stream);
+    return c.w_rows ? launch_shape<4, 2, 2, 2, false, true>(c, stream) : launch_shape<4, 2, 2, 4, false, false>(c, stream);
+  }
+  if (!c.y_bf16) return c.w_rows ? launch_shape<2, 2, 2, 2, true, true>(c, stream) : launch_shape<2, 2, 2, 2, true, false>(c, stream);
+  return c.w_rows ? launch_shape<2, 2, 2, 2, false, true>(c, stream) : launch_shape<2, 2, 2, 2, false, false>(c, stream);
 }
 
 }  // namespace splr
