@@ -33,15 +33,17 @@ struct Fp8Call {
 struct Fp8Plan {
   bool quantize;  // X is quantised to the workspace first
   int rows, tokens;
+  int stages = 2;  // of tiles of 128 x 128: steps in LDS
 };
 bool plan_fp8(const Fp8Call& c, Fp8Plan* plan);
 size_t fp8_workspace_bytes(const Fp8Call& c, const Fp8Plan& plan);
 hipError_t launch_fp8(const Fp8Call& c, const Fp8Plan& plan, hipStream_t stream);
 // Its parts
-bool fp8_few_grid_fits(const Fp8Call& c);
-hipError_t launch_fp8_few(const Fp8Call& c, hipStream_t stream);
+bool fp8_few_grid_fits(const Fp8Call& c, int tokens);  // 16 or 32
+bool fp8_few_quantizes(const Fp8Call& c, int tokens);  // X's tile fits its LDS
+hipError_t launch_fp8_few(const Fp8Call& c, int tokens, hipStream_t stream);
 bool fp8_tile_grid_fits(const Fp8Call& c, int rows, int tokens);
-hipError_t launch_fp8_tile(const Fp8Call& c, int rows, hipStream_t stream);
+hipError_t launch_fp8_tile(const Fp8Call& c, int rows, int stages, hipStream_t stream);
 
 // X [rows][cols] to e4m3 in blocks of 1 x 128 or 128 x 128 (`block`); the launch limits of that.
 bool fp8_quantize_grids_fit(int64_t rows, int64_t cols, bool block, bool transposed);
@@ -79,22 +81,19 @@ __device__ __forceinline__ bf16x8_t widen_e4m3(u32x2_t v) {
   return as_bf16x8(w);
 }
 
-// Sixteen consecutive entries of X as float32
+// Eight consecutive entries of X as float32
 template <bool BF16>
-__device__ __forceinline__ void load16(const void* p, size_t at, float (&v)[16]) {
+__device__ __forceinline__ void load8(const void* p, size_t at, float (&v)[8]) {
   if constexpr (BF16) {
+    const u32x4_t w = *(const u32x4_t*)((const uint16_t*)p + at);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const u32x4_t w = ((const u32x4_t*)((const uint16_t*)p + at))[h];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[8 * h + 2 * i] = __uint_as_float(w[i] << 16);
-        v[8 * h + 2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-      }
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
     }
   } else {
 #pragma unroll
-    for (int h = 0; h < 4; ++h) {
+    for (int h = 0; h < 2; ++h) {
       const f32x4_t w = ((const f32x4_t*)((const float*)p + at))[h];
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[4 * h + i] = w[i];

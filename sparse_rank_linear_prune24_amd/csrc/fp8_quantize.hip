@@ -15,23 +15,7 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(const void* __restri
   if (row >= rows) return;
   float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
   const bool here = col < cols;
-  if (here) {
-    if constexpr (BF16) {
-      const u32x4_t w = *(const u32x4_t*)((const uint16_t*)X + row * cols + col);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[2 * i] = __uint_as_float(w[i] << 16);
-        v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-      }
-    } else {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const f32x4_t w = ((const f32x4_t*)((const float*)X + row * cols + col))[h];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[4 * h + i] = w[i];
-      }
-    }
-  }
+  if (here) load8<BF16>(X, row * cols + col, v);
   uint32_t m = largest_bits(v);
   if (__any(m >= kInfBits)) m = drop_infinite(v);
 #pragma unroll

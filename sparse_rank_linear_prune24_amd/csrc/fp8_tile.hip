@@ -1,10 +1,22 @@
-// The 8-bit product in large workgroup tiles, both operands through LDS.
+// The 8-bit product in workgroup tiles of 128 x 128 and 256 x 256, both operands through LDS.
 //
 //   acc[n][m] += sx[m][kb] sw[n][kb] p,   p = sum over the block's 128 columns of W[n][k] X[m][k]
 //
-// A step is one block of 128 columns: rows of 128 bytes of W and X go straight from memory to LDS (no registers between),
-// two steps deep, and from there to the matrix instructions as fragments of 32 x 32. p starts from zero in every step, so
-// that the scales can be applied to it in float32: 16 multiply-adds for every 32 x 32 x 128 products.
+// A step is one block of 128 columns: rows of 128 bytes of W and X go straight from memory to LDS (no registers between), two
+// or four steps deep, and from there to the matrix instructions as fragments of 32 x 32. p starts from zero in every step, so
+// that the scales can be applied to it in float32: 16 multiply-adds a lane for every 32 x 32 x 128 products.
+//
+// With a bfloat16 Y the products run on the e4m3 matrix instructions. Of each eight consecutive products these keep what lies
+// within 2^-13 of the largest (measured: one 2^-14 of it is lost), which rounding Y to 2^-9 hides; a float32 Y would show it, so
+// for that both operands are widened to bfloat16, exactly, on their way from LDS, and the sums of a block are float32 sums, at
+// half the rate.
+//
+// What bounds it, 8192 x 4096 -> 14336, bfloat16 Y, 483 us (2.0 PFLOP/s; the matrix instructions alone with their multiply-adds
+// run at 4.4): the power limit holds the clock at 1.75 GHz, of whose cycles the matrix cores take 58 %; the same loop without
+// loads from memory takes 385 us, the epilogue 40 us. 16 x 16 x 128 instructions instead of 32 x 32 x 64: 605 us at the time
+// when these took 550; four multiply-adds an instruction leave no room between dependent ones. One word of each line fetched two
+// steps ahead (for L2): 8 % slower, the requests are what is short. A float32 Y: 926 us (1.04 PFLOP/s), bound by the conversions
+// (32 for every 8 matrix instructions, 1.5 times the time of other vector instructions) beside them.
 //
 // Rows lie 128 bytes apart in LDS without padding (a direct load writes 64 consecutive pieces of 16 bytes); piece c of row r
 // stands at place c ^ (r / 2 % 8) of its row, so that the 16 lanes that read 16 bytes each at a time (lanes 0 .. 3, 12 .. 15,
@@ -34,9 +46,9 @@ __device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t rs, uint8_t* 
 // is free; it tells the compiler what is outstanding.
 template <int LATER>
 __device__ __forceinline__ void step_barrier() {
-  static_assert(LATER < 16, "the wait's low bits");
+  static_assert(LATER < 64, "the wait's bits");
   asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"i"(LATER) : "memory");
-  __builtin_amdgcn_s_waitcnt(0x0070 | LATER);
+  __builtin_amdgcn_s_waitcnt(0x0070 | (LATER & 15) | (LATER >> 4) << 14);
 }
 
 // Fragments of 32 rows x 128 columns. A lane's part is of row lane % 32: pieces 2 h, 2 h + 1, 2 h + 4 and 2 h + 5
@@ -82,25 +94,26 @@ __device__ __forceinline__ Sum multiply(const Fragment<true>& a, const Fragment<
   return p;
 }
 
-// WR x WT waves, each NR x NT fragments: a workgroup tile of 32 WR NR rows of W x 32 WT NT tokens.
-template <int WR, int WT, int NR, int NT>
+// WR x WT waves, each NR x NT fragments: a workgroup tile of 32 WR NR rows of W x 32 WT NT tokens; STAGES steps' operands in LDS.
+template <int WR, int WT, int NR, int NT, int STAGES>
 struct Shape {
   static constexpr int kWaves = WR * WT, kThreads = kWaves * kWave, kWaveRows = NR * 32, kWaveTokens = NT * 32;
   static constexpr int kRows = WR * kWaveRows, kTokens = WT * kWaveTokens;
-  static constexpr int kStage = (kRows + kTokens) * kBlockK;  // LDS of a step's operands: two of them, then
-  static constexpr int kScales = (kRows + kTokens) * 4;       // four steps' scales, and what nobody reads
-  static constexpr int kSpare = 2 * kStage + 4 * kScales, kAll = kSpare + kWaves * 256;
+  static constexpr int kStage = (kRows + kTokens) * kBlockK;  // LDS of a step's operands: STAGES of them, then
+  static constexpr int kScales = (kRows + kTokens) * 4;       // the scales of twice as many steps, and what nobody reads
+  static constexpr int kSlots = STAGES <= 2 ? 4 : 8;
+  static constexpr int kScales0 = STAGES * kStage, kSpare = kScales0 + kSlots * kScales, kAll = kSpare + kWaves * 256;
   static constexpr int kPitch = kWaveRows + 4, kEpilogue = kWaves * 32 * kPitch * 4;  // floats of a token's row in the epilogue
   static constexpr int kLds = kAll > kEpilogue ? kAll : kEpilogue;
 };
 
-template <int WR, int WT, int NR, int NT, bool WIDE, bool W_ROWS, bool EXPERTS>
+template <int WR, int WT, int NR, int NT, int STAGES, bool WIDE, bool W_ROWS, bool EXPERTS>
 __global__ __launch_bounds__(WR * WT * kWave, 2) void fp8_tile_kernel(
     const uint8_t* __restrict__ X, const float* __restrict__ x_scales, const uint8_t* __restrict__ W,
     const float* __restrict__ w_scales, Epilogue ep, void* Y, int past_caches, int M, int K, int n_out, int tiles_n, Groups groups) {
-  using S = Shape<WR, WT, NR, NT>;
+  using S = Shape<WR, WT, NR, NT, STAGES>;
   constexpr int BN = S::kRows, BM = S::kTokens, kWaves = S::kWaves;
-  __shared__ __align__(1024) uint8_t lds[S::kLds];
+  extern __shared__ __align__(1024) uint8_t lds[];  // S::kLds, of which the compiler would take fewer waves for granted
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int KB = (K + kBlockK - 1) / kBlockK;
   // Each XCD (own L2) runs a contiguous range of the tiles, four token tiles at a time row block by row block, so that it
@@ -145,15 +158,15 @@ __global__ __launch_bounds__(WR * WT * kWave, 2) void fp8_tile_kernel(
   const int scales_first = (of_x ? wave : wave - BM / 64) * 64, scales_end = (of_x ? rows_m : rows_n) * 4;
   const float* const scales0 = of_x ? x_scales + row0 + m0 : w_scale + n0;
   const int64_t scales_step = of_x ? all_rows : n_out;
-  const int scales_ring = of_x || of_w ? 3 : 0;
-  const int scales_to = of_x   ? 2 * S::kStage + scales_first * 4
-                        : of_w ? 2 * S::kStage + kScaleW + scales_first * 4
+  const int scales_ring = of_x || of_w ? S::kSlots - 1 : 0;
+  const int scales_to = of_x   ? S::kScales0 + scales_first * 4
+                        : of_w ? S::kScales0 + kScaleW + scales_first * 4
                                : S::kSpare + wave * 256;
   const int scales_off = of_x || of_w ? (scales_first + lane) * 4 : kAway;
-  // Load d of a step. Of a step past the last nothing is read, and zeros are written. No branches, here and in the loop:
+  // Load d of step kb, to a stage. Of a step past the last nothing is read, and zeros are written. No branches, here and in the loop:
   // across them the compiler would move the multiply-adds away from the matrix instructions that they belong to.
   constexpr int kLoads = kLoadsW + kLoadsX + 1;
-  auto load = [&](int kb, int d) __attribute__((always_inline)) {
+  auto load = [&](int kb, int stage, int d) __attribute__((always_inline)) {
     if (d == kLoads - 1) {
       const __amdgpu_buffer_rsrc_t rs =
           __builtin_amdgcn_make_buffer_rsrc((void*)(scales0 + kb * scales_step), (short)0, scales_end, kBuffer);
@@ -165,7 +178,7 @@ __global__ __launch_bounds__(WR * WT * kWave, 2) void fp8_tile_kernel(
       const int rows = of_w ? rows_n : rows_m;
       const __amdgpu_buffer_rsrc_t rs =
           __builtin_amdgcn_make_buffer_rsrc((void*)(of_w ? w0 : x0), (short)0, rows * K, kBuffer);
-      load_to_lds<16>(rs, lds + (kb & 1) * S::kStage + (of_w ? 0 : kX) + (wave + t) * 1024,
+      load_to_lds<16>(rs, lds + stage * S::kStage + (of_w ? 0 : kX) + (wave + t) * 1024,
                       __umul24(min(l_row + 8 * t, rows - 1), K) + (kb * kBlockK + l_col < K ? l_col : kAway),
                       kb * kBlockK);
     }
@@ -183,22 +196,22 @@ __global__ __launch_bounds__(WR * WT * kWave, 2) void fp8_tile_kernel(
 
   // The steps. p of a fragment is added to the sums while the next one's matrix instructions run; the last one's in the next
   // step. A step's last LDS reads lie before its last column of fragments: there the waves meet, the step's place in LDS takes
-  // the loads of the step after next, and the next one's first fragments are read as the present ones are done with.
+  // the loads of the step STAGES on, and the next one's first fragments are read as the present ones are done with.
   using F = Fragment<WIDE>;
   constexpr int kBlocks = NR * NT;
   static_assert(NT % 2 == 0, "rings with constant indexes");
   F a[NR], b[2];
   Raw raw;  // WIDE: of the next column of fragments
   Sum acc[NR][NT], p[2];
-  float s[2] = {0.0f, 0.0f};  // scales of this column's tokens, and the last's
+  float s[2] = {0.0f, 0.0f}, s_next;  // scales of this column's tokens and the last's; the next one's as read
 #pragma unroll
   for (int i = 0; i < NR; ++i)
 #pragma unroll
     for (int j = 0; j < NT; ++j) acc[i][j] = Sum{};
   p[0] = p[1] = Sum{};
   const float* const sw_block = w_scale + (size_t)(min(n0 + wave_n, n_out - 1) / 128) * KB;
-  const float* const x_scale = (const float*)(lds + 2 * S::kStage) + wave_m + lane % 32;
-  const float* const r_scale = (const float*)(lds + 2 * S::kStage + kScaleW) + wave_n;
+  const float* const x_scale = (const float*)(lds + S::kScales0) + wave_m + lane % 32;
+  const float* const r_scale = (const float*)(lds + S::kScales0 + kScaleW) + wave_n;
   auto read_now = [&](const uint8_t* rows, F& f) __attribute__((always_inline)) {
     if constexpr (WIDE) {
       Raw r;
@@ -213,7 +226,7 @@ __global__ __launch_bounds__(WR * WT * kWave, 2) void fp8_tile_kernel(
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
       f32x4_t by = {s[j & 1], s[j & 1], s[j & 1], s[j & 1]};
-      if constexpr (W_ROWS) by *= *(const f32x4_t*)(r_scale + (kb & 3) * (S::kScales / 4) + i * 32 + first_row(lane, g));
+      if constexpr (W_ROWS) by *= *(const f32x4_t*)(r_scale + (kb & (S::kSlots - 1)) * (S::kScales / 4) + i * 32 + first_row(lane, g));
 #pragma unroll
       for (int k = 0; k < 4; ++k) acc[i][j][4 * g + k] = fmaf(p[t & 1][4 * g + k], by[k], acc[i][j][4 * g + k]);
     }
@@ -221,17 +234,22 @@ __global__ __launch_bounds__(WR * WT * kWave, 2) void fp8_tile_kernel(
   // A step's loads are spread over kSpread fragments from its last column on, so that no wave waits with its matrix
   // instructions behind a queue of loads.
   constexpr int kSpread = NR + 1, kEachLoads = (kLoads + kSpread - 1) / kSpread;
-  static_for<kLoads>([&](auto d) __attribute__((always_inline)) { load(0, decltype(d)::value); });
   constexpr int kFirst = NR * kEachLoads < kLoads ? NR * kEachLoads : kLoads;  // issued in the step itself
-  static_for<kFirst>([&](auto d) __attribute__((always_inline)) { load(1, decltype(d)::value); });
-  step_barrier<kFirst>();
+  static_for<STAGES>([&](auto st) __attribute__((always_inline)) {
+    constexpr int step = decltype(st)::value;
+    static_for<step + 1 < STAGES ? kLoads : kFirst>([&](auto d) __attribute__((always_inline)) { load(step, step, decltype(d)::value); });
+  });
+  step_barrier<(STAGES - 2) * kLoads + kFirst>();
   float sw = W_ROWS ? 1.0f : sw_block[0];
 #pragma unroll
   for (int i = 0; i < NR; ++i) read_now(lds + (wave_n + i * 32) * kBlockK, a[i]);
   read_now(lds + kX + wave_m * kBlockK, b[0]);
+  s_next = x_scale[0];
+  int now_at = 0, last_at = STAGES - 1;  // stages of this step and the last one
   for (int kb = 0; kb < KB; ++kb) {
-    const uint8_t* const x = lds + (kb & 1) * S::kStage + kX + wave_m * kBlockK;
-    const uint8_t* const next = lds + (~kb & 1) * S::kStage;  // after the last step: of what lies there
+    const int next_at = now_at + 1 < STAGES ? now_at + 1 : 0;
+    const uint8_t* const x = lds + now_at * S::kStage + kX + wave_m * kBlockK;
+    const uint8_t* const next = lds + next_at * S::kStage;  // after the last step: of what lies there
     const float sw_next = W_ROWS ? 1.0f : sw_block[min(kb + 1, KB - 1)];
     static_for<kBlocks>([&](auto tt) __attribute__((always_inline)) {
       constexpr int t = decltype(tt)::value, i = t % NR, j = t / NR;
@@ -240,7 +258,7 @@ __global__ __launch_bounds__(WR * WT * kWave, 2) void fp8_tile_kernel(
           if constexpr (WIDE) read(x + (j + 1) * 32 * kBlockK, raw);
           else read(x + (j + 1) * 32 * kBlockK, b[(j + 1) & 1]);
         } else {
-          step_barrier<0>();
+          step_barrier<(STAGES - 2) * kLoads>();  // the next step's loads have arrived
           if constexpr (WIDE) read(next + kX + wave_m * kBlockK, raw);
           else read(next + kX + wave_m * kBlockK, b[0]);
         }
@@ -249,12 +267,16 @@ __global__ __launch_bounds__(WR * WT * kWave, 2) void fp8_tile_kernel(
       constexpr int kFrom = kTurn * kEachLoads;
       constexpr int kCount = kFrom >= kLoads ? 0 : kLoads - kFrom < kEachLoads ? kLoads - kFrom : kEachLoads;
       static_for<kCount>([&](auto d) __attribute__((always_inline)) {
-        load(t >= kBlocks - NR ? kb + 2 : kb + 1, kFrom + decltype(d)::value);
+        constexpr bool kNow = t >= kBlocks - NR;
+        load(kNow ? kb + STAGES : kb + STAGES - 1, kNow ? now_at : last_at, kFrom + decltype(d)::value);
       });
+      if constexpr (i == 0) {
+        s[j & 1] = s_next * sw;
+        s_next = x_scale[((j + 1 < NT ? kb : kb + 1) & (S::kSlots - 1)) * (S::kScales / 4) + 32 * ((j + 1) % NT)];
+      }
       const Sum now = multiply(a[i], b[j & 1]);
       add(t > 0 ? kb : kb - 1, std::integral_constant<int, (t + kBlocks - 1) % kBlocks>{});
       p[t & 1] = now;
-      if constexpr (i == 0) s[j & 1] = x_scale[(kb & 3) * (S::kScales / 4) + 32 * j] * sw;
       if constexpr (WIDE && i == NR - 1) b[(j + 1) & 1].take(raw);
       constexpr int kInstructions = WIDE ? 8 : 2, kEach = WIDE ? 4 : 8;
 #pragma unroll
@@ -267,6 +289,8 @@ __global__ __launch_bounds__(WR * WT * kWave, 2) void fp8_tile_kernel(
       if constexpr (j == NT - 1) read_now(next + (wave_n + i * 32) * kBlockK, a[i]);
     });
     sw = sw_next;
+    last_at = now_at;
+    now_at = next_at;
   }
   add(KB - 1, std::integral_constant<int, kBlocks - 1>{});
   // The result through LDS, 32 tokens at a time in a part of each wave's own, so that loads and stores of the epilogue take
@@ -340,15 +364,15 @@ int64_t tile_blocks(const Fp8Call& c, int tokens) {
   return c.offsets ? most_group_tiles(c.M, c.experts, tokens) : ceil_div(c.M, tokens);
 }
 
-template <int WR, int WT, int NR, int NT, bool WIDE, bool W_ROWS>
+template <int WR, int WT, int NR, int NT, int STAGES, bool WIDE, bool W_ROWS>
 hipError_t launch_shape(const Fp8Call& c, hipStream_t stream) {
-  using S = Shape<WR, WT, NR, NT>;
+  using S = Shape<WR, WT, NR, NT, STAGES>;
   const int tiles_n = (int)ceil_div(c.n_out, S::kRows);
   const dim3 grid((unsigned)(8 * ceil_div(tiles_n * tile_blocks(c, S::kTokens), 8)));
   const Groups groups{c.offsets, (int)c.experts, (int)c.M};
   const int past = (double)c.M * c.n_out * (WIDE ? 4 : 2) > kNonTemporalYBytes;
-  const auto kernel = c.offsets ? fp8_tile_kernel<WR, WT, NR, NT, WIDE, W_ROWS, true> : fp8_tile_kernel<WR, WT, NR, NT, WIDE, W_ROWS, false>;
-  kernel<<<grid, dim3(S::kThreads), 0, stream>>>((const uint8_t*)c.X, c.x_scales, c.W, c.w_scales, c.ep, c.Y,
+  const auto kernel = c.offsets ? fp8_tile_kernel<WR, WT, NR, NT, STAGES, WIDE, W_ROWS, true> : fp8_tile_kernel<WR, WT, NR, NT, STAGES, WIDE, W_ROWS, false>;
+  kernel<<<grid, dim3(S::kThreads), S::kLds, stream>>>((const uint8_t*)c.X, c.x_scales, c.W, c.w_scales, c.ep, c.Y,
                                                  past, (int)c.M, (int)c.n_in, (int)c.n_out, tiles_n, groups);
   return hipGetLastError();
 }
@@ -359,13 +383,14 @@ bool fp8_tile_grid_fits(const Fp8Call& c, int rows, int tokens) {
   return tile_blocks(c, tokens) * ceil_div(c.n_out, rows) < (int64_t(1) << 23);
 }
 
-hipError_t launch_fp8_tile(const Fp8Call& c, int rows, hipStream_t stream) {
-  if (rows == 256) {
-    if (!c.y_bf16) return c.w_rows ? launch_shape<4, 2, 2, 2, true, true>(c, stream) : launch_shape<4, 2, 2, 2, true, false>(c, stream);
-    return c.w_rows ? launch_shape<4, 2, 2, 2, false, true>(c, stream) : launch_shape<4, 2, 2, 4, false, false>(c, stream);
-  }
-  if (!c.y_bf16) return c.w_rows ? launch_shape<2, 2, 2, 2, true, true>(c, stream) : launch_shape<2, 2, 2, 2, true, false>(c, stream);
-  return c.w_rows ? launch_shape<2, 2, 2, 2, false, true>(c, stream) : launch_shape<2, 2, 2, 2, false, false>(c, stream);
+hipError_t launch_fp8_tile(const Fp8Call& c, int rows, int stages, hipStream_t stream) {
+  if (rows == 256) return launch_shape<4, 2, 2, 4, 2, false, false>(c, stream);
+  const auto launch = [&](auto st) {
+    constexpr int kStages = decltype(st)::value;
+    if (!c.y_bf16) return c.w_rows ? launch_shape<2, 2, 2, 2, kStages, true, true>(c, stream) : launch_shape<2, 2, 2, 2, kStages, true, false>(c, stream);
+    return c.w_rows ? launch_shape<2, 2, 2, 2, kStages, false, true>(c, stream) : launch_shape<2, 2, 2, 2, kStages, false, false>(c, stream);
+  };
+  return stages == 2 ? launch(std::integral_constant<int, 2>{}) : launch(std::integral_constant<int, 4>{});
 }
 
 }  // namespace splr

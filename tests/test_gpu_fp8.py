@@ -68,7 +68,7 @@ def test_every_rounding():
 # M, n_in, n_out
 SIZES = [(1, 32, 1), (1, 4096, 4096), (2, 96, 203), (13, 1056, 203), (16, 2048, 1024), (17, 160, 130), (33, 512, 1003), (64, 1056, 520),
          (100, 2080, 1003), (250, 1056, 4090), (256, 4096, 1024), (333, 1056, 1003), (700, 992, 2050), (1000, 4096, 2048),
-         (2100, 544, 4096)]
+         (1100, 288, 4096), (2100, 544, 4096), (3000, 512, 4500)]
 
 
 def narrow(M, n_out, n_in, dtype, y_dtype, experts=None):
@@ -91,7 +91,7 @@ def test_linear(M, n_in, n_out, dtype, y_dtype):
     assert torch.equal(Y, binding.linear_fp8(X, w.W, w.s, x_scales=scales, y_dtype=y_dtype))
 
 
-@pytest.mark.parametrize("M,n_in,n_out", [(5, 160, 203), (48, 512, 516), (300, 1056, 1003), (600, 512, 2048)])
+@pytest.mark.parametrize("M,n_in,n_out", [(5, 160, 203), (48, 512, 516), (300, 1056, 1003), (600, 512, 2048), (2100, 544, 4098)])
 @pytest.mark.parametrize("y_dtype", [bf, f32])
 def test_epilogue(M, n_in, n_out, y_dtype):
     w = Weight(n_out, n_in, 7, std=0.2)
@@ -118,7 +118,7 @@ def test_epilogue(M, n_in, n_out, y_dtype):
 
 # rows, experts, n_in, n_out
 EXPERTS = [(0, 3, 64, 40), (1, 5, 64, 40), (64, 32, 2048, 1024), (13, 4, 1056, 40), (100, 60, 96, 203), (500, 6, 512, 776), (700, 4, 1056, 1003),
-           (3000, 7, 544, 1024), (2000, 1, 512, 512), (600, 1000, 64, 50)]
+           (3000, 7, 544, 1024), (2500, 4, 1056, 4090), (2000, 1, 512, 512), (600, 1000, 64, 50)]
 
 
 def offsets_of(rows, E, seed, before=0, behind=0):
@@ -211,7 +211,7 @@ def test_gradients(M, n_in, n_out, dtype):
 
 def test_not_finite():
     """NaN and infinities in X make their rows NaN, in W (NaN codes) their columns, and nothing else; on every kernel."""
-    for M, n_out in ((3, 64), (20, 200), (200, 1003), (1500, 2048)):
+    for M, n_out in ((3, 64), (20, 200), (200, 1003), (600, 520), (1500, 2048), (2100, 4096)):
         n_in = 544
         w = Weight(n_out, n_in, 28)
         codes = w.codes.copy()
@@ -227,7 +227,7 @@ def test_not_finite():
 
 def test_scales_of_one_row():
     """w_block_rows 1 and 128 with the same scales give the same sums."""
-    for M, n_in, n_out in ((9, 256, 300), (200, 544, 1003), (1500, 544, 2048)):
+    for M, n_in, n_out in ((9, 256, 300), (200, 544, 1003), (300, 544, 2048), (1100, 288, 4096), (3000, 512, 4500)):
         w = Weight(n_out, n_in, 30)
         X, x64 = floats((M, n_in), bf, 31)
         by_row = w.s.repeat_interleave(128, 0)[:n_out].T.contiguous()

@@ -256,6 +256,25 @@ def test_binding_of_products(host_as_device):
                      dict(bias=z(N)), dict(W=W), dict(W=z(E + 1, N, K, dtype=e4m3)), dict(w_scales=s), dict(w_scales=z(E, N, 2))])
 
 
+def test_every_kernel_has_a_size():
+    """The sizes that the GPU tests run take every kernel of the products."""
+    from tests.test_gpu_fp8 import EXPERTS, SIZES
+    want = {(16, 16), (16, 32), (128, 128), (256, 256)}
+    for E in (None, 1):
+        for y_dtype in (bf, f32):
+            sizes = [(M, n_out, n_in, None) for M, n_in, n_out in SIZES] if E is None else [(M, n_out, n_in, e) for M, e, n_in, n_out in EXPERTS if M]
+            tiles = {binding.linear_fp8_tile(M, n_out, n_in, bf, y_dtype, e) for M, n_out, n_in, e in sizes}
+            assert tiles == (want if y_dtype is bf else want - {(256, 256)}), (E, y_dtype, tiles)
+    # tiles of 128 with two steps in LDS (more of them than CUs) and with four, for both types
+    for y_dtype in (bf, f32):
+        of = [-(-M // 128) * -(-n_out // 128) for M, n_in, n_out in SIZES if binding.linear_fp8_tile(M, n_out, n_in, bf, y_dtype) == (128, 128)]
+        assert min(of) <= 256 < max(of)
+    # X quantised by the workgroups (no workspace) and by a launch of its own, by the few-token kernels
+    needs = {binding.linear_fp8_workspace_bytes(M, n_out, n_in, bf, bf) > 0 for M, n_in, n_out in SIZES
+             if binding.linear_fp8_tile(M, n_out, n_in, bf, bf)[0] == 16}
+    assert needs == {True, False}
+
+
 def test_sizes_that_the_types_share():
     assert binding.SLOTS_MAX == 64 and binding.SPLR_E4M3 == 2
     assert binding.linear_fp8_workspace_bytes(16, 64, 64, e4m3, bf) == 0
