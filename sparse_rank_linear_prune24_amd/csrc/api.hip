@@ -504,9 +504,8 @@ splr_status_t splr_tokens_dispatch(const void* ids, int32_t id_bytes, int64_t T,
     for (int j = 0; j < i; ++j)
       if (out[i].meets(out[j])) return SPLR_ERR_OVERLAP;
   }
-  const hipError_t e = splr::launch_tokens_sort(ids, id_bytes == 8, N, n_experts, offsets, positions, workspace, stream);
-  if (e != hipSuccess || !copy || T == 0) return from_hip(e);
-  return from_hip(splr::launch_tokens_gather(X, T, D, size, positions, slots, Xs, N, stream));
+  return from_hip(splr::launch_tokens_dispatch(ids, id_bytes == 8, T, slots, n_experts, offsets, positions, workspace,
+                                               copy ? X : nullptr, D, size, Xs, stream));
 }
 
 splr_status_t splr_tokens_gather(const void* X, int64_t T, int64_t D, splr_dtype_t dtype, const int32_t* positions,

@@ -14,7 +14,9 @@ bf, f32 = torch.bfloat16, torch.float32
 SIZES = [
     (1, 8, 32, 2048, bf, torch.int64, 0.0), (1, 1, 1, 1, f32, torch.int32, 0.0), (3, 1, 2, 7, bf, torch.int32, 1.0),
     (16, 8, 32, 2048, bf, torch.int64, 0.0), (333, 3, 60, 1003, f32, torch.int32, 0.1), (100, 5, 7, 1411, bf, torch.int64, 0.9),
-    (1365, 3, 5, 40, f32, torch.int32, 0.0), (1366, 3, 5, 40, f32, torch.int32, 0.0),      # 4095 and 4098 slots
+    (341, 3, 5, 40, f32, torch.int32, 0.0), (342, 3, 5, 40, f32, torch.int32, 0.0),        # 1023 and 1026 slots: one workgroup, two
+    (32, 8, 1024, 128, bf, torch.int32, 0.1), (33, 8, 9, 128, bf, torch.int32, 0.0), (37, 2, 12, 5000, f32, torch.int64, 0.1),
+    (8193, 2, 8, 24, bf, torch.int32, 0.0),                                                # the most slots of one launch are 16384
     (2048, 2, 1024, 72, bf, torch.int64, 0.3), (4097, 1, 256, 100, bf, torch.int32, 0.0), (700, 64, 300, 33, bf, torch.int32, 0.2),
     (8192, 2, 8, 512, bf, torch.int64, 0.0), (20011, 3, 1024, 8, f32, torch.int64, 0.05),
 ]
@@ -223,7 +225,7 @@ def test_offsets_past_31_bits():
 
 
 def test_streams_graphs_and_replays():
-    T, k, E, D = 3000, 2, 12, 256
+    T, k, E, D = 9000, 2, 12, 256
     ids, X, weights = routes(T, k, E, 0.1, 20), rows(T, D, bf, 21), torch.rand(T, k).cuda()
     out, Y = torch.zeros(T * k, D, dtype=bf, device="cuda"), torch.zeros(T, D, dtype=bf, device="cuda")
     offsets, positions = torch.zeros(E + 1, dtype=torch.int32, device="cuda"), torch.zeros(T, k, dtype=torch.int32, device="cuda")
