@@ -7,12 +7,13 @@
 namespace splr {
 
 // The path with the least predicted time, from whole-call times on MI355X (256 CUs) over n_in 1056 .. 14336, n_out 1003 ..
-// 14336, 16 .. 4096 rows, and 8 and 60 experts of 2 .. 300 rows, X in bfloat16. A step is a block of 128 columns. Examples, us by
+// 14336, 16 .. 4096 rows, and 4 .. 60 experts of 2 .. 380 rows, X in bfloat16. A step is a block of 128 columns. Examples, us by
 // path (few-token kernel with 16 / 32 tokens a workgroup; tiles of 128 x 128 with two / four steps in LDS; of 256 x 256):
 //   4096 -> 4096, bfloat16 Y     16 rows  10 /  11 / 30 / 26 / 49     128 rows  29 / 21 / 32 / 27 / 50
 //                               512 rows  95 /  63 / 34 / 29 / 53    4096 rows    -  / - / 96 / 119 / 79
 //   4096 -> 14336               256 rows 152 /  97 / 34 / 30 / 50    2048 rows    -  / - / 178 / 190 / 134
 //   14336 -> 1024               256 rows  42 /  31 / 94 / 73 / 149
+//   96 -> 13120                 224 rows  92 with 16 tokens a workgroup
 //   8 experts 4096 -> 4096, 8 rows each 46 / 46 / 51 / 44 / 59; 300 rows each 726 / 473 / 98 / 91 / 75
 // float32 Y (no tiles of 256): 4096 -> 4096, 512 rows 94 / 62 / 42 / 41, 4096 rows -/-/ 150 / 176.
 bool plan_fp8(const Fp8Call& c, Fp8Plan* plan) {
@@ -23,10 +24,12 @@ bool plan_fp8(const Fp8Call& c, Fp8Plan* plan) {
   };
   const double read = active * c.n_out * c.n_in / 4.0e6 + 8;  // W at 4 TB/s, us
   const double never = 1e30;
-  const auto few = [&](int tokens, double fixed, double each) {
-    return fp8_few_grid_fits(c, tokens) ? std::max(fixed + each * blocks(tokens) * ceil_div(c.n_out, 16) * KB, read) : never;
+  // a workgroup's part of a tile of 16 rows: its meeting and store, and the blocks of its tokens
+  const auto few = [&](int tokens, double fixed, double tile, double block) {
+    if (!fp8_few_grid_fits(c, tokens)) return never;
+    return std::max(fixed + blocks(tokens) * ceil_div(c.n_out, 16) * (tile + block * KB), read);
   };
-  const double t16 = few(16, 6.5, 0.35e-3), t32 = few(32, 8.6, 0.41e-3);
+  const double t16 = few(16, 6.5, 5.5e-3, 0.24e-3), t32 = few(32, 8.6, 5e-3, 0.33e-3);
   // one workgroup a CU: four steps in LDS hide its latencies; more: two steps, so that a CU takes two
   const double tiles = blocks(128) * ceil_div(c.n_out, 128);
   const int stages = tiles <= 256 ? 4 : 2;

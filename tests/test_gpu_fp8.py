@@ -118,7 +118,8 @@ def test_epilogue(M, n_in, n_out, y_dtype):
 
 # rows, experts, n_in, n_out
 EXPERTS = [(0, 3, 64, 40), (1, 5, 64, 40), (64, 32, 2048, 1024), (13, 4, 1056, 40), (100, 60, 96, 203), (500, 6, 512, 776), (700, 4, 1056, 1003),
-           (3000, 7, 544, 1024), (2500, 4, 1056, 4090), (2000, 1, 512, 512), (600, 1000, 64, 50)]
+           (3000, 7, 544, 1024), (2500, 4, 1056, 4090), (2000, 1, 512, 512), (600, 1000, 64, 50),
+           (200, 4, 1056, 1003)]
 
 
 def offsets_of(rows, E, seed, before=0, behind=0):
