@@ -527,12 +527,14 @@ splr_status_t splr_tokens_combine_backward(const void* dY, const void* Z, int64_
  *         number), added up in float32, block after block; everything after in float32, rounded once.
  *         With a float32 Y the sums within a block are float32 too. With a bfloat16 Y large calls form them
  *         on the 8-bit matrix instructions, which of every eight products keep what is within 2^-13 of the
- *         largest: up to 2^-12 of the sum of absolute products, a tenth of bfloat16's own rounding on
- *         ordinary data. NaN entries make their row or column of Y NaN. Bitwise reproducible run to run.
+ *         largest: less than 2^-10 of the sum of absolute products is lost (8 x 2^-13; measured 2^-12.5 at
+ *         worst and 2^-15 of the result's norm on ordinary data, where rounding Y gives 2^-9). NaN entries
+ *         make their row or column of Y NaN. Bitwise reproducible run to run.
  * splr_linear_fp8_experts -- the same for rows grouped by expert, as splr_linear_experts: W [n_experts][n_out][n_in],
  *         w_scales and bias one expert after the other, offsets [n_experts + 1] int32 on the device, M may be 0.
- * splr_linear_fp8_tile -- which kernel sizes take, as its workgroup tile (n_experts 0: splr_linear_fp8). For
- *         tests and timing; the choice is no part of the contract.
+ * splr_linear_fp8_tile -- which kernel sizes take with w_block_rows 128, as its workgroup tile (n_experts 0:
+ *         splr_linear_fp8); w_block_rows 1 has no tile of 256 x 256. For tests and timing; the choice is no
+ *         part of the contract.
  * Errors: as splr_linear_fused and splr_linear_experts; w_block_rows other than 1 and 128 -> SPLR_ERR_SHAPE.
  */
 splr_status_t splr_fp8_quantize(const void* X, int64_t rows, int64_t cols, splr_dtype_t dtype,

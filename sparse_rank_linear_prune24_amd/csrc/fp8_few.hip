@@ -5,10 +5,10 @@
 //
 // Reading W bounds this kernel. Each wave has a ring of its own in LDS, AHEAD blocks deep, that loads fill without registers
 // between and without barriers, from one tile into the next: whole lines of 128 bytes of eight rows at a time (one row 14336 ->
-// 4096: 15.2 us; with fragments read to registers, 64 bytes of 16 rows at a time, 17.7). Both operands become bfloat16 in registers (exact), so that the sums over
-// a block are float32 sums on the bfloat16 matrix cores, whose time does not show here. X that is not held in 8 bits yet is
-// quantised by the workgroup, into LDS, while the first of W arrives: a launch of its own would cost more than the few rows that
-// a tile has.
+// 4096: 15.2 us; with fragments read to registers, 64 bytes of 16 rows at a time, 17.7). Both operands become bfloat16 in
+// registers (exact), so that the sums over a block are float32 sums on the bfloat16 matrix cores, whose time does not show here.
+// X that is not held in 8 bits yet is quantised by the workgroup, into LDS, while the first of W arrives: a launch of its own
+// would cost more than the few rows that a tile has.
 #include "fp8.hpp"
 #include "tile_common.hpp"
 
