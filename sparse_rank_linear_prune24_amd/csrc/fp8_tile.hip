@@ -180,7 +180,7 @@ __global__ __launch_bounds__(WR * WT * kWave, 2) void fp8_tile_kernel(
           __builtin_amdgcn_make_buffer_rsrc((void*)(of_w ? w0 : x0), (short)0, rows * K, kBuffer);
       load_to_lds<16>(rs, lds + stage * S::kStage + (of_w ? 0 : kX) + (wave + t) * 1024,
                       __umul24(min(l_row + 8 * t, rows - 1), K) + (kb * kBlockK + l_col < K ? l_col : kAway),
-                      kb * kBlockK);
+                      min(kb, KB - 1) * kBlockK);  // an offset past the descriptor's size could wrap in its bounds check
     }
   };
   static_assert(!W_ROWS || BM / 64 + BN / 64 <= kWaves, "a wave for each 64 scales");
