@@ -273,3 +273,23 @@ def test_graph_and_stream():
     run(side)
     side.synchronize()
     assert torch.equal(Y, want[0]) and torch.equal(Z, want[1])
+
+
+@pytest.mark.parametrize("M,n_in,n_out", [(600_000, 64, 4100), (70_001, 32768, 24)])
+def test_offsets_past_31_bits(M, n_in, n_out):
+    """Y, and X with its quantised form, of more than 2^31 entries: rows of the start, the end and around 2^31 entries."""
+    w = Weight(n_out, n_in, 70)
+    few, x64 = floats((97, n_in), bf, 71)     # rows repeat, 97 of them
+    X = few.repeat(-(-M // 97), 1)[:M].contiguous()
+    assert max(M * n_in, M * n_out) > 1 << 31
+    middle = (1 << 31) // max(n_in, n_out)
+    at = np.unique(np.concatenate([np.arange(40), middle + np.arange(-20, 20), M - 1 - np.arange(300)]))
+    thin = narrow(M, n_out, n_in, bf, bf)
+    want, bound = product64(held(x64), w.values, bf, thin)
+    offsets = torch.tensor([0, 5, M], dtype=torch.int32, device="cuda")
+    pair = torch.stack([w.W.view(torch.uint8)] * 2).view(E4M3), torch.stack([w.s] * 2)
+    for Y in (binding.linear_fp8(X, w.W, w.s, y_dtype=bf), binding.linear_fp8_experts(X, offsets, *pair, y_dtype=bf)):
+        check(Y[torch.from_numpy(at).cuda()], want[at % 97], bound[at % 97], f"{M} {n_in} {n_out}")
+        for lo in range(0, M, 97 * 1000):     # every row is the row of its kind, bit for bit
+            part = Y[lo:lo + 97 * 1000]
+            assert torch.equal(part, Y[:97].repeat(-(-len(part) // 97), 1)[:len(part)])
