@@ -80,12 +80,22 @@ __device__ __forceinline__ void with_flag(bool flag, F&& f) {
 // Four consecutive entries of a float32 or bfloat16 array, as loaded (a bfloat16 quad fills two words):
 // those from entry `at` on, of which only the first `left` exist (the others read as 0). vec: all four
 // do, aligned to four entries.
+// The loads of four entries take any entry's address, as gfx950 does. ANY: the caller's may be less aligned than the four.
+template <typename T, bool ANY>
+struct AtEntry {
+  typedef T type __attribute__((aligned(2)));
+};
+template <typename T>
+struct AtEntry<T, false> {
+  typedef T type;
+};
+template <bool ANY = false>
 __device__ __forceinline__ u32x4_t load_raw4(const void* p, size_t at, bool bf16, bool vec, int left) {
   u32x4_t v = {0, 0, 0, 0};
   if (bf16) {
     const uint16_t* h = (const uint16_t*)p + at;
     if (vec) {
-      const u32x2_t w = *(const u32x2_t*)h;
+      const u32x2_t w = *(const typename AtEntry<u32x2_t, ANY>::type*)h;
       v[0] = w[0];
       v[1] = w[1];
     } else {
@@ -96,7 +106,7 @@ __device__ __forceinline__ u32x4_t load_raw4(const void* p, size_t at, bool bf16
   } else {
     const uint32_t* f = (const uint32_t*)p + at;
     if (vec) {
-      v = *(const u32x4_t*)f;
+      v = *(const typename AtEntry<u32x4_t, ANY>::type*)f;
     } else {
 #pragma unroll
       for (int e = 0; e < 4; ++e)
@@ -121,14 +131,14 @@ __device__ __forceinline__ uint32_t round_bf16x2(float a, float b) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{a, b}, bf16x2_t));
 }
 
-template <bool NT>
+template <bool NT, bool ANY = false>
 __device__ __forceinline__ void store4(void* p, size_t at, bool bf16, bool vec, int left, f32x4_t v) {
   if (bf16) {
     uint16_t* h = (uint16_t*)p + at;
     const u32x2_t w = u32x2_t{round_bf16x2(v[0], v[1]), round_bf16x2(v[2], v[3])};
     if (vec) {
-      if constexpr (NT) __builtin_nontemporal_store(w, (u32x2_t*)h);
-      else *(u32x2_t*)h = w;
+      if constexpr (NT) __builtin_nontemporal_store(w, (typename AtEntry<u32x2_t, ANY>::type*)h);
+      else *(typename AtEntry<u32x2_t, ANY>::type*)h = w;
     } else {
 #pragma unroll
       for (int e = 0; e < 4; ++e)
@@ -137,8 +147,8 @@ __device__ __forceinline__ void store4(void* p, size_t at, bool bf16, bool vec, 
   } else {
     float* f = (float*)p + at;
     if (vec) {
-      if constexpr (NT) __builtin_nontemporal_store(v, (f32x4_t*)f);
-      else *(f32x4_t*)f = v;
+      if constexpr (NT) __builtin_nontemporal_store(v, (typename AtEntry<f32x4_t, ANY>::type*)f);
+      else *(typename AtEntry<f32x4_t, ANY>::type*)f = v;
     } else {
 #pragma unroll
       for (int e = 0; e < 4; ++e)

@@ -168,13 +168,13 @@ __global__ __launch_bounds__(kFewThreads) void fp8_few_kernel(
     // the epilogue's operands first: one wave finishes a fragment, another one in the next tile
     const int n0 = tile * 16, out_row = n0 + 4 * quad, left = n_out - out_row;
     const int mine = (wave - turn_of_sums * NT) & (kFewWaves - 1);
-    const bool finishes = mine < NT && m0 + 16 * mine + sub < rows && left > 0, vec = left >= 4 && n_out % 4 == 0;
+    const bool finishes = mine < NT && m0 + 16 * mine + sub < rows && left > 0, vec = left >= 4;
     const size_t at = (row0 + m0 + 16 * mine + sub) * n_out + out_row;
     u32x4_t bias = {0, 0, 0, 0}, gate = bias, residual = bias;
     if (finishes) {
-      if (ep.bias) bias = load_raw4(ep.bias, e * n_out + out_row, y_bf16, vec, left);
-      if (ep.gate) gate = load_raw4(ep.gate, at, y_bf16, vec, left);
-      if (ep.residual) residual = load_raw4(ep.residual, at, y_bf16, vec, left);
+      if (ep.bias) bias = load_raw4<true>(ep.bias, e * n_out + out_row, y_bf16, vec, left);
+      if (ep.gate) gate = load_raw4<true>(ep.gate, at, y_bf16, vec, left);
+      if (ep.residual) residual = load_raw4<true>(ep.residual, at, y_bf16, vec, left);
     }
 #pragma unroll
     for (int j = 0; j < NT; ++j) acc[j] = f32x4_t{0, 0, 0, 0};
@@ -229,7 +229,7 @@ __global__ __launch_bounds__(kFewThreads) void fp8_few_kernel(
       f32x4_t sum = *(const f32x4_t*)&parts[0][mine][sub * kPitch + 4 * quad];
 #pragma unroll
       for (int v = 1; v < kFewWaves; ++v) sum += *(const f32x4_t*)&parts[v][mine][sub * kPitch + 4 * quad];
-      store4<false>(Y, at, y_bf16, vec, left, finish4(sum, widen4(bias, y_bf16), ep, widen4(gate, y_bf16), widen4(residual, y_bf16)));
+      store4<false, true>(Y, at, y_bf16, vec, left, finish4(sum, widen4(bias, y_bf16), ep, widen4(gate, y_bf16), widen4(residual, y_bf16)));
     }
     ++turn_of_sums;
   }

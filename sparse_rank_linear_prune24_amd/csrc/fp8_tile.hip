@@ -300,9 +300,9 @@ __global__ __launch_bounds__(WR * WT * kWave, 2) void fp8_tile_kernel(
   constexpr bool kBf16 = !WIDE;  // Y's type
   float* const mine = (float*)lds + wave * 32 * S::kPitch;
   const int c = lane % kLanes * 4, n = n0 + wave_n + c, left = n_out - n;
-  const bool vec = n_out % 4 == 0 && left >= 4;
-  const f32x4_t bias = ep.bias && left > 0 ? load4(ep.bias, e * n_out + n, kBf16, vec, left) : f32x4_t{0, 0, 0, 0};
-  // whole: every entry of the wave's exists, four aligned; past: stores that pass the caches
+  const bool vec = left >= 4;  // at any alignment (462 rows 3840 -> 2381 with gate and residual: whole call 44.7 -> 32 us)
+  const f32x4_t bias = ep.bias && left > 0 ? widen4(load_raw4<true>(ep.bias, e * n_out + n, kBf16, vec, left), kBf16) : f32x4_t{0, 0, 0, 0};
+  // whole: every entry of the wave's exists; past: stores that pass the caches
   const auto finish = [&](auto whole, auto past) __attribute__((always_inline)) {
     static_for<NT>([&](auto jj) __attribute__((always_inline)) {
       constexpr int j = decltype(jj)::value;
@@ -317,7 +317,7 @@ __global__ __launch_bounds__(WR * WT * kWave, 2) void fp8_tile_kernel(
 #pragma unroll
         for (int r = 0; r < kRounds; ++r) {
           size_t at;
-          if (place(r, at)) v[r] = load_raw4(p, at, kBf16, decltype(whole)::value || vec, left);
+          if (place(r, at)) v[r] = load_raw4<true>(p, at, kBf16, decltype(whole)::value || vec, left);
           else v[r] = u32x4_t{0, 0, 0, 0};
         }
       };
@@ -349,13 +349,13 @@ __global__ __launch_bounds__(WR * WT * kWave, 2) void fp8_tile_kernel(
 #pragma unroll
       for (int r = 0; r < kRounds; ++r) {
         size_t at;
-        if (place(r, at)) store4<decltype(past)::value>(Y, at, kBf16, decltype(whole)::value || vec, left, y[r]);
+        if (place(r, at)) store4<decltype(past)::value, true>(Y, at, kBf16, decltype(whole)::value || vec, left, y[r]);
       }
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     });
   };
   // A Y too large for the caches goes past them: the rows of X and W that later tiles read stay there instead.
-  if (n_out % 4 != 0 || n0 + wave_n + S::kWaveRows > n_out || m0 + wave_m + S::kWaveTokens > M) finish(std::false_type{}, std::false_type{});
+  if (n0 + wave_n + S::kWaveRows > n_out || m0 + wave_m + S::kWaveTokens > M) finish(std::false_type{}, std::false_type{});
   else if (past_caches) finish(std::true_type{}, std::true_type{});
   else finish(std::true_type{}, std::false_type{});
 }
