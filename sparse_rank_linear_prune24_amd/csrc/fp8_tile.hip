@@ -275,7 +275,8 @@ __global__ __launch_bounds__(WR * WT * kWave, 2) void fp8_tile_kernel(
         s_next = x_scale[((j + 1 < NT ? kb : kb + 1) & (S::kSlots - 1)) * (S::kScales / 4) + 32 * ((j + 1) % NT)];
       }
       const Sum now = multiply(a[i], b[j & 1]);
-      add(t > 0 ? kb : kb - 1, std::integral_constant<int, (t + kBlocks - 1) % kBlocks>{});
+      // The first step's first addition, of p = 0, takes step 0's scales: a place that this call has not filled can hold NaN.
+      add(t > 0 ? kb : max(kb - 1, 0), std::integral_constant<int, (t + kBlocks - 1) % kBlocks>{});
       p[t & 1] = now;
       if constexpr (WIDE && i == NR - 1) b[(j + 1) & 1].take(raw);
       constexpr int kInstructions = WIDE ? 8 : 2, kEach = WIDE ? 4 : 8;
