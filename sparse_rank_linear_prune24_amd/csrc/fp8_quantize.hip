@@ -30,7 +30,8 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(const void* __restri
   }
 }
 
-// The rest: one workgroup a tile of 128 x 128, a thread two columns (64 apart) of 32 rows.
+// The rest: one workgroup a tile of 128 x 128, a thread two columns (64 apart) of 32 rows. The tiles are numbered row after row in
+// the grid's x: its y ends at 65535, and there may be 2^17 tiles in either direction.
 // TRANSPOSED: Q [cols][pitch], pitch = rows rounded up to 32, zeros past the rows. BLOCK: one scale for the tile.
 template <bool BF16, bool TRANSPOSED, bool BLOCK>
 __global__ __launch_bounds__(256) void quantize_tile_kernel(const void* __restrict__ X, int64_t rows, int64_t cols,
@@ -38,7 +39,9 @@ __global__ __launch_bounds__(256) void quantize_tile_kernel(const void* __restri
                                                             float* __restrict__ scales) {
   __shared__ uint32_t largest[4][128];
   const int c = threadIdx.x & 63, g = threadIdx.x >> 6;
-  const int64_t r0 = blockIdx.y * (int64_t)128, c0 = blockIdx.x * (int64_t)128, row0 = r0 + 32 * g;
+  const unsigned row_tiles = (unsigned)((rows + 127) / 128), col_tiles = (unsigned)((cols + 127) / 128);
+  const unsigned row_tile = blockIdx.x / col_tiles, col_tile = blockIdx.x - row_tile * col_tiles;
+  const int64_t r0 = row_tile * (int64_t)128, c0 = col_tile * (int64_t)128, row0 = r0 + 32 * g;
   float v[2][32];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
@@ -72,9 +75,9 @@ __global__ __launch_bounds__(256) void quantize_tile_kernel(const void* __restri
     const float s = block_scale(__uint_as_float(m[h])), inv = 1.0f / s;
     if constexpr (BLOCK) {
       if (threadIdx.x == 0 && h == 0)
-        scales[TRANSPOSED ? (size_t)blockIdx.x * gridDim.y + blockIdx.y : (size_t)blockIdx.y * gridDim.x + blockIdx.x] = s;
+        scales[TRANSPOSED ? (size_t)col_tile * row_tiles + row_tile : (size_t)row_tile * col_tiles + col_tile] = s;
     } else {
-      if (g == 0) scales[(size_t)blockIdx.y * cols + col] = s;
+      if (g == 0) scales[(size_t)row_tile * cols + col] = s;
     }
     if constexpr (TRANSPOSED) {
       if (row0 >= pitch) continue;
@@ -99,7 +102,7 @@ __global__ __launch_bounds__(256) void quantize_tile_kernel(const void* __restri
 dim3 rows_grid(int64_t rows, int64_t cols) {
   return dim3((unsigned)ceil_div(rows, 4), (unsigned)ceil_div(cols, 4 * kBlockK));
 }
-dim3 tile_grid(int64_t rows, int64_t cols) { return dim3((unsigned)ceil_div(cols, 128), (unsigned)ceil_div(rows, 128)); }
+dim3 tile_grid(int64_t rows, int64_t cols) { return dim3((unsigned)(ceil_div(cols, 128) * ceil_div(rows, 128))); }
 
 }  // namespace
 
