@@ -520,9 +520,11 @@ splr_status_t splr_tokens_combine_backward(const void* dY, const void* Z, int64_
  *   workspace  splr_linear_fp8_workspace_bytes() bytes (n_experts 0), clobbered. Two calls that may run
  *              at the same time need one each.
  * Its gradients are products of the same kind. With dY [M][n_out]: dX = dY W is the product of dY and W
- * quantised with block_rows 128, transposed 1 (the same blocks); dW = dY^T X that of dY and X, both
- * quantised with block_rows 1, transposed 1 (M becomes the reduction dimension, w_block_rows is 1);
- * residual adds to a gradient that is there.
+ * quantised with block_rows 128, transposed 1 (the same blocks); n_out is its reduction dimension, so
+ * where that is no multiple of 32 the caller holds dY as [M][n_out rounded up to 32], zeros behind its
+ * rows, as W transposed has them. dW = dY^T X is the product of dY and X, both quantised with block_rows 1,
+ * transposed 1 (M becomes the reduction dimension, w_block_rows is 1; M and n_out are any); residual adds
+ * to a gradient that is there.
  * Arithmetic: the sum over each block of 128 columns, times both scales (their product has to be a float32
  *         number), added up in float32, block after block; everything after in float32, rounded once.
  *         With a float32 Y the sums within a block are float32 too. With a bfloat16 Y large calls form them

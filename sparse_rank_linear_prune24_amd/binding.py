@@ -964,7 +964,8 @@ def linear_fp8(X: torch.Tensor, W: torch.Tensor, w_scales: torch.Tensor, x_scale
     """Y [M, n_out] of y_dtype = act(X W^T + bias) * gate + residual with W [n_out, n_in] in e4m3 (splr_linear_fp8). w_scales
     [ceil(n_out/128), ceil(n_in/128)] (blocks of 128 x 128) or [ceil(n_in/128), n_out] (of 1 x 128). X [M, n_in] float32 or
     bfloat16 is quantised by the call; in e4m3 it comes with x_scales [ceil(n_in/128), M]. bias [n_out], gate and residual
-    [M, n_out] of y_dtype; `out` may be gate or residual itself. The workspace holds linear_fp8_workspace_bytes()."""
+    [M, n_out] of y_dtype; `out` may be gate or residual itself. The workspace holds linear_fp8_workspace_bytes(). The gradient dX =
+    dY W is linear_fp8 of dY and fp8_quantize(w, 128, transposed=True), dY's rows padded with zeros to a multiple of 32."""
     return _fp8_call(X, None, W, w_scales, x_scales, bias, activation, gate, residual, y_dtype, out, workspace, stream)
 
 
