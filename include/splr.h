@@ -524,7 +524,8 @@ splr_status_t splr_tokens_combine_backward(const void* dY, const void* Z, int64_
  * where that is no multiple of 32 the caller holds dY as [M][n_out rounded up to 32], zeros behind its
  * rows, as W transposed has them. dW = dY^T X is the product of dY and X, both quantised with block_rows 1,
  * transposed 1 (M becomes the reduction dimension, w_block_rows is 1; M and n_out are any); residual adds
- * to a gradient that is there.
+ * to a gradient that is there. There is no form of dW by expert: a caller takes each expert's rows of dY and X
+ * by offsets that the host knows, from a 16-byte aligned start on, and an expert without rows has none.
  * Arithmetic: the sum over each block of 128 columns, times both scales (their product has to be a float32
  *         number), added up in float32, block after block; everything after in float32, rounded once.
  *         With a float32 Y the sums within a block are float32 too. With a bfloat16 Y large calls form them

@@ -37,3 +37,25 @@ def test_rows_gradient_of_any_width(M, n_in, n_out, dtype, y_dtype):
     check(binding.linear_fp8(padded, Wt, wt_s, y_dtype=y_dtype), want, bound, "dX")
     q, s = binding.fp8_quantize(padded)                  # quantised once, for several products
     check(binding.linear_fp8(q, Wt, wt_s, x_scales=s, y_dtype=y_dtype), want, bound, "dX of codes")
+
+
+@pytest.mark.parametrize("n_in,n_out", [(64, 40), (96, 203)])
+def test_expert_weight_gradients_from_host_offsets(n_in, n_out):
+    """An expert's dW takes its rows by offsets that the host knows; rows whose start is not 16-byte aligned have to be copied."""
+    ends, dtype = [0, 37, 37, 150, 301], bf
+    dY, y64 = floats((301, n_out), dtype, 3, std=1e-3)
+    X, x64 = floats((301, n_in), dtype, 4, outliers=2)
+    for a, b in zip(ends, ends[1:]):
+        if a == b:
+            with pytest.raises(binding.SplrError, match="SPLR_ERR_(SHAPE|NULL)"):   # no rows, no product: this dW is 0
+                binding.fp8_quantize(dY[a:b], transposed=True)
+            continue
+        part = dY[a:b]
+        if part.data_ptr() % 16:
+            with pytest.raises(binding.SplrError, match="SPLR_ERR_ALIGN"):
+                binding.fp8_quantize(part, transposed=True)
+            part = part.clone()
+        dq, ds = binding.fp8_quantize(part, transposed=True)
+        xq, xs = binding.fp8_quantize(X[a:b], transposed=True)
+        want, bound = product64(held(y64[a:b].T), held(x64[a:b].T), f32, False)
+        check(binding.linear_fp8(dq, xq, xs, x_scales=ds), want, bound, f"rows {a} .. {b}")
