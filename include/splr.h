@@ -459,6 +459,8 @@ splr_status_t splr_linear_fused_tile(int64_t M, int64_t n_experts, int64_t n_out
  * position outside 0 .. rows - 1 counts as -1. Two slots with one position (no dispatch gives them) leave
  * that row of Xs or dZ unspecified. T may be 0 (row buffers may be NULL then; offsets become 0), and rows too.
  * Types: rows of SPLR_FP32 or SPLR_BF16; dispatch and gather, which copy, also of SPLR_E4M3. D is any.
+ *         Rows of SPLR_E4M3 are codes alone: their scales, [ceil(D/128)][T], move as float32 rows
+ *         [T][ceil(D/128)] of a gather of their own, transposed before and behind it.
  * Arithmetic: float32 sums in the order of the slots (dweights: a fixed order of the columns), rounded
  *         once. Weights multiply in float32, so a row of infinity or NaN reaches its own token only.
  *         Bitwise reproducible run to run.
