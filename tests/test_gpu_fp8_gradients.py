@@ -59,3 +59,18 @@ def test_expert_weight_gradients_from_host_offsets(n_in, n_out):
         xq, xs = binding.fp8_quantize(X[a:b], transposed=True)
         want, bound = product64(held(y64[a:b].T), held(x64[a:b].T), f32, False)
         check(binding.linear_fp8(dq, xq, xs, x_scales=ds), want, bound, f"rows {a} .. {b}")
+
+
+@pytest.mark.parametrize("M,n_in,n_out", [(777, 515, 2050), (400, 1600, 1003)])
+def test_weight_gradient_on_tiles(M, n_in, n_out):
+    """dW = dY^T X at sizes that the tile kernels take, with scales as far apart as tokens' gradients and outlier channels make them."""
+    spread_of = torch.exp2(torch.arange(n_out, device="cuda") % 13 - 6.0)
+    dY, _ = floats((M, n_out), f32, 5, std=1e-3)
+    dY = (dY * spread_of).to(bf)
+    X, x64 = floats((M, n_in), bf, 6, outliers=8)
+    dq, ds = binding.fp8_quantize(dY, transposed=True)
+    xq, xs = binding.fp8_quantize(X, transposed=True)
+    for y_dtype in (f32, bf):
+        assert binding.linear_fp8_tile(n_out, n_in, dq.shape[1], dq.dtype, y_dtype) == (128, 128)
+        want, bound = product64(held(dY.double().cpu().numpy().T), held(x64.T), y_dtype, y_dtype is bf)
+        check(binding.linear_fp8(dq, xq, xs, x_scales=ds, y_dtype=y_dtype), want, bound, f"dW {y_dtype}")
