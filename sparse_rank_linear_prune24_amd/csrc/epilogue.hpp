@@ -77,10 +77,8 @@ __device__ __forceinline__ void with_flag(bool flag, F&& f) {
   else f(std::false_type{});
 }
 
-// Four consecutive entries of a float32 or bfloat16 array, as loaded (a bfloat16 quad fills two words):
-// those from entry `at` on, of which only the first `left` exist (the others read as 0). vec: all four
-// do, aligned to four entries.
-// The loads of four entries take any entry's address, as gfx950 does. ANY: the caller's may be less aligned than the four.
+// T, of four entries, as it is loaded and stored. ANY: from any entry's address on, which gfx950 takes, or
+// aligned to T.
 template <typename T, bool ANY>
 struct AtEntry {
   typedef T type __attribute__((aligned(2)));
@@ -89,6 +87,9 @@ template <typename T>
 struct AtEntry<T, false> {
   typedef T type;
 };
+// Four consecutive entries of a float32 or bfloat16 array, as loaded (a bfloat16 quad fills two words):
+// those from entry `at` on, of which only the first `left` exist (the others read as 0). vec: all four
+// do; without ANY they are then aligned to four entries.
 template <bool ANY = false>
 __device__ __forceinline__ u32x4_t load_raw4(const void* p, size_t at, bool bf16, bool vec, int left) {
   u32x4_t v = {0, 0, 0, 0};
