@@ -15,8 +15,12 @@ namespace splr {
 namespace {
 
 constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / kWave;
-// Rows are copied by the sort's launch where one workgroup sorts and there is as little to copy
-constexpr int kCopySlots = 256, kCopyBytes = 64 << 10;
+// Rows are copied by the sort's launch where one workgroup sorts and there is as little to copy: its 16 waves take a row at a
+// time. Whole calls in a graph, 32 experts, bfloat16 rows, copied by the sort / by a launch of their own, us:
+//   128 columns   8 slots 3.8 / 4.8    64 slots 4.8 / 5.3    128 slots 6.0 / 5.3    256 slots 8.3 / 5.4
+//   1024 columns  8 slots 4.0 / 4.7    32 slots (64 KiB) 4.8 / 5.2    64 slots 5.7 / 5.2
+//   2048 columns  8 slots 4.3 / 4.8    16 slots (64 KiB) 4.7 / 5.2    32 slots 5.7 / 5.3      7168 columns  8 slots 5.8 / 5.2
+constexpr int kCopySlots = 64, kCopyBytes = 64 << 10;
 
 // A slot's expert, -1 when its id names none.
 __device__ __forceinline__ int expert_of(const void* ids, int wide, int64_t i, int experts) {
