@@ -30,7 +30,9 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(const void* __restri
   }
 }
 
-// The rest: one workgroup a tile of 128 x 128, a thread two columns (64 apart) of 32 rows. The tiles are numbered row after row in
+// The rest: one workgroup a tile of 128 x 128, a thread two columns (64 apart) of 32 rows. Bound by its narrow accesses, entry
+// by entry from X, to Q one byte at a time or, transposed, 16 bytes of 64 rows: bfloat16 in blocks of 128 x 128 4096 x 4096
+// 18.7 us (2.7 TB/s; transposed 16.4), 14336 x 4096 60.9 (56.1); of 1 x 128 transposed 2048 x 4096 9.0. The tiles are numbered row after row in
 // the grid's x: its y ends at 65535, and there may be 2^17 tiles in either direction.
 // TRANSPOSED: Q [cols][pitch], pitch = rows rounded up to 32, zeros past the rows. BLOCK: one scale for the tile.
 template <bool BF16, bool TRANSPOSED, bool BLOCK>

@@ -11,11 +11,12 @@
 // of it) hides. A float32 Y would show it, so for that both operands are widened to bfloat16, exactly, on their way from LDS, and
 // the sums of a block are float32 sums, at half the rate.
 //
-// What bounds it, 8192 x 4096 -> 14336, bfloat16 Y, 483 us (2.0 PFLOP/s; the matrix instructions alone with their multiply-adds
-// run at 4.4): the power limit holds the clock at 1.75 GHz, of whose cycles the matrix cores take 58 %; the same loop without
-// loads from memory takes 385 us, the epilogue 40 us. 16 x 16 x 128 instructions instead of 32 x 32 x 64: 605 us at the time
+// What bounds it, 8192 x 4096 -> 14336, bfloat16 Y, 480 us (2.0 PFLOP/s; the matrix instructions alone with their multiply-adds
+// run at 4.4): the power limit holds the clock at 1.7 GHz, of whose cycles the matrix cores take 59 %; the same loop without
+// its loads from memory takes 403 us, and about 70 us are the fills and epilogues of seven rounds of tiles, which n_in does not
+// change (n_in 2048: 274 us, 8192: 865). 16 x 16 x 128 instructions instead of 32 x 32 x 64: 605 us at the time
 // when these took 550; four multiply-adds an instruction leave no room between dependent ones. One word of each line fetched two
-// steps ahead (for L2): 8 % slower, the requests are what is short. A float32 Y: 926 us (1.04 PFLOP/s), bound by the conversions
+// steps ahead (for L2): 8 % slower, the requests are what is short. A float32 Y: 905 us (1.06 PFLOP/s), bound by the conversions
 // (32 for every 8 matrix instructions, 1.5 times the time of other vector instructions) beside them.
 //
 // Rows lie 128 bytes apart in LDS without padding (a direct load writes 64 consecutive pieces of 16 bytes); piece c of row r
