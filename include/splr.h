@@ -465,7 +465,7 @@ splr_status_t splr_linear_fused_tile(int64_t M, int64_t n_experts, int64_t n_out
  *         once. Weights multiply in float32, so a row of infinity or NaN reaches its own token only.
  *         Bitwise reproducible run to run.
  * Errors: NULL pointer -> SPLR_ERR_NULL; slots outside 1 .. SPLR_SLOTS_MAX, T not below 2^24, T * slots
- *         or rows above 2^28, D outside 1 .. 2^20, rows of 2^36 entries or more, n_experts outside
+ *         or rows above 2^28, D outside 1 .. 2^20, rows of more than 2^36 entries, n_experts outside
  *         1 .. SPLR_EXPERTS_MAX -> SPLR_ERR_SHAPE; id_bytes or dtype -> SPLR_ERR_DTYPE; rows not 16-byte
  *         aligned, the rest not to its entries -> SPLR_ERR_ALIGN; workspace too small ->
  *         SPLR_ERR_WORKSPACE; an output that overlaps an operand or another output (but as said) ->
